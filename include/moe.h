@@ -282,6 +282,149 @@ moe_status moe_dense_forward(const moe_dense_config* cfg, const uint16_t* x,
                              const uint16_t* w_down, uint16_t* y, void* ws, size_t ws_bytes,
                              hipStream_t stream);
 
+/* ---- Linear and grouped products, and their gradients ---------------------
+ * The layer's matrix products as operators of their own, for the dense
+ * projections around it and for training: a linear map with bias, activation
+ * and residual in its epilogue, the same map grouped by expert with ragged
+ * group sizes, SwiGLU between an expert's products, and the gradients of all
+ * three.  A routed layer in training is moe_route, moe_permute, grouped gate
+ * and up products of the gathered tokens, moe_swiglu_forward, and the grouped
+ * down product; its backward pass is the same calls backwards.
+ *
+ * Conventions and errors as above, and:
+ *   - bf16 operands, exact products, fp32 accumulation; bias and its gradient
+ *     are fp32.  y and dw are bf16 or fp32 (y_dtype, dw_dtype), rounded once.
+ *   - in_features and out_features are multiples of 8, from 8 to 65536; rows
+ *     (tokens) up to 2^26, any number of them, 0 included; rows * in_features,
+ *     rows * out_features and num_groups * in_features * out_features are below
+ *     2^35.
+ *   - Results do not depend on timing (fixed summation order, no atomics).
+ *   - Nothing is allocated and nothing copied to the host: every call can be
+ *     captured in a HIP graph.  The workspace is taken with any contents and
+ *     written before it is read; calls that share one must be ordered. */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0            */
+  MOE_ACT_GELU = 2,      /* z Phi(z), Phi the normal CDF (erf) */
+  MOE_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  MOE_ACT_SILU = 4       /* z / (1 + e^-z)                     */
+} moe_activation;
+
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype;
+
+typedef struct {
+  int64_t tokens;       /* T >= 0                                              */
+  int32_t in_features;  /* K                                                   */
+  int32_t out_features; /* F                                                   */
+  int32_t activation;   /* MOE_ACT_*                                           */
+  int32_t y_dtype;      /* MOE_DTYPE_* of y                                    */
+  int32_t dw_dtype;     /* MOE_DTYPE_* of dw                                   */
+  int32_t accumulate;   /* nonzero: the backward pass adds to dw and dbias     */
+} moe_linear_config;
+
+/* Device workspace that moe_linear_forward and moe_linear_backward need (one
+ * size serves both); 0 for an invalid configuration.  It depends on the
+ * current device's number of compute units. */
+size_t moe_linear_workspace_size(const moe_linear_config* cfg);
+
+/* z = x W^T + bias;  y = act(z) + residual.
+ *   x         [T][K] bf16;  w [F][K] bf16
+ *   bias      [F] fp32 or NULL;  residual [T][F] bf16 or NULL
+ *   y         out [T][F], y_dtype
+ *   z         out [T][F] bf16, the pre-activation that the backward pass of an
+ *             activation needs, or NULL.  y is formed from the unrounded z. */
+moe_status moe_linear_forward(const moe_linear_config* cfg, const uint16_t* x, const uint16_t* w,
+                              const float* bias, const uint16_t* residual, void* y, uint16_t* z,
+                              void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradients of moe_linear_forward for dy, the gradient of y (the residual's
+ * gradient is dy itself):
+ *   dz = dy act'(z);  dx = dz W;  dw (+)= dz^T x;  dbias (+)= sum_t dz
+ *   dy     [T][F] bf16
+ *   z      [T][F] bf16 as moe_linear_forward left it (not read, and may be
+ *          NULL, with MOE_ACT_NONE)
+ *   dz     out [T][F] bf16 (not written, and may be NULL, with MOE_ACT_NONE,
+ *          where it is dy).  It is rounded to bf16 once, and dx and dw are
+ *          formed from it as rounded; dbias sums the unrounded values.
+ *   dx     out [T][K] bf16, or NULL;  dw out [F][K], dw_dtype, or NULL;
+ *   dbias  out [F] fp32, or NULL
+ * x is not read, and may be NULL, when dw is NULL; w likewise when dx is NULL.
+ * With tokens == 0, dw and dbias are set to zero (nothing is added when
+ * accumulate is set). */
+moe_status moe_linear_backward(const moe_linear_config* cfg, const uint16_t* dy, const uint16_t* z,
+                               const uint16_t* x, const uint16_t* w, uint16_t* dz, uint16_t* dx,
+                               void* dw, float* dbias, void* ws, size_t ws_bytes,
+                               hipStream_t stream);
+
+typedef struct {
+  int64_t rows;         /* P >= 0: rows of y, dy and dx                         */
+  int64_t x_rows;       /* rows of x when row_ids is given, else P              */
+  int32_t num_groups;   /* E, 1 .. 1024                                         */
+  int32_t in_features;  /* K                                                    */
+  int32_t out_features; /* F                                                    */
+  int32_t row_div;      /* >= 1: row r reads row row_ids[r] / row_div of x      */
+  int32_t y_dtype;      /* MOE_DTYPE_* of y                                     */
+  int32_t dw_dtype;     /* MOE_DTYPE_* of dw                                    */
+  int32_t accumulate;   /* nonzero: the backward pass adds to dw and dbias      */
+  int32_t reserved;     /* must be 0                                            */
+} moe_grouped_config;
+
+size_t moe_grouped_workspace_size(const moe_grouped_config* cfg);
+
+/* Products grouped by expert: rows offsets[e] .. offsets[e+1] - 1 belong to
+ * group e, and y[r] = W_e x[src(r)] + bias_e.
+ *   x        [x_rows][K] bf16
+ *   row_ids  [P] int32 or NULL: src(r) = row_ids[r] / row_div, so that
+ *            moe_permute's sorted_pairs with row_div = top_k read the token
+ *            rows in place; NULL: src(r) = r.  A row whose source lies outside
+ *            x reads as zeros.  x_rows * K below 2013265920 when it is given.
+ *   offsets  [E+1] int32 on the device, ascending (moe_permute's); groups may
+ *            be empty, and values are clamped to [0, P].  Rows outside
+ *            [offsets[0], offsets[E]) are left as they were.
+ *   w        [E][F][K] bf16;  bias [E][F] fp32 or NULL
+ *   y        out [P][F], y_dtype */
+moe_status moe_grouped_forward(const moe_grouped_config* cfg, const uint16_t* x,
+                               const int32_t* row_ids, const int32_t* offsets, const uint16_t* w,
+                               const float* bias, void* y, void* ws, size_t ws_bytes,
+                               hipStream_t stream);
+
+/* Gradients of moe_grouped_forward:
+ *   dx[r] = W_e^T dy[r];  dw[e] (+)= sum_{r in e} dy[r] x[src(r)]^T;
+ *   dbias[e] (+)= sum_{r in e} dy[r]
+ *   dy     [P][F] bf16
+ *   dx     out [P][K] bf16, one row per row of y (with row_ids, the gradient
+ *          of a row of x is the sum over the rows that read it), or NULL
+ *   dw     out [E][F][K], dw_dtype, or NULL;  dbias out [E][F] fp32, or NULL
+ * An empty group's dw and dbias are zero (nothing is added when accumulate is
+ * set).  x and row_ids are not read when dw is NULL, w not when dx is NULL. */
+moe_status moe_grouped_backward(const moe_grouped_config* cfg, const uint16_t* dy,
+                                const uint16_t* x, const int32_t* row_ids, const int32_t* offsets,
+                                const uint16_t* w, uint16_t* dx, void* dw, float* dbias, void* ws,
+                                size_t ws_bytes, hipStream_t stream);
+
+typedef struct {
+  int64_t rows;     /* >= 0                                                     */
+  int32_t inter;    /* I, a multiple of 8                                       */
+  int32_t ld;       /* row stride of gate, up, dgate and dup in elements: a
+                       multiple of 8, >= inter (2 I for the halves of one
+                       product's rows); 0 = inter                              */
+  float limit;      /* swiglu_limits[layer]; <= 0: no clamp                     */
+  int32_t reserved; /* must be 0                                                */
+} moe_swiglu_config;
+
+/* h = SiLU(min(g, L)) * clamp(u, -L, L), the activation of moe_forward's
+ * experts.  gate, up [rows] x ld bf16; h out [rows][I] bf16.  rows * ld is
+ * below 2^35. */
+moe_status moe_swiglu_forward(const moe_swiglu_config* cfg, const uint16_t* gate,
+                              const uint16_t* up, uint16_t* h, hipStream_t stream);
+
+/* dgate and dup (row stride ld) for dh [rows][I] bf16.  The clamp passes the
+ * gradient of values up to and including its limit.  h (out [rows][I], or
+ * NULL) is recomputed on the way, for a backward pass that did not keep it. */
+moe_status moe_swiglu_backward(const moe_swiglu_config* cfg, const uint16_t* dh,
+                               const uint16_t* gate, const uint16_t* up, uint16_t* dgate,
+                               uint16_t* dup, uint16_t* h, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

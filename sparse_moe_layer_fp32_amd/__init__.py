@@ -57,6 +57,58 @@ def make_dense_config(tokens, hidden=4096, inter=11264, swiglu_limit=0.0) -> moe
     return moe_dense_config(int(tokens), int(hidden), int(inter), float(swiglu_limit), 0)
 
 
+ACTIVATIONS = ("none", "relu", "gelu", "gelu_tanh", "silu")  # MOE_ACT_*
+DTYPES = ("bf16", "f32")                                      # MOE_DTYPE_*
+
+
+def _index(names, value, what):
+    if value not in names:
+        raise ValueError(f"{what} {value!r} is none of {', '.join(names)}")
+    return names.index(value)
+
+
+class moe_linear_config(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("in_features", ctypes.c_int32),
+                ("out_features", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
+def make_linear_config(tokens, in_features, out_features, activation="none", y_dtype="bf16",
+                       dw_dtype="f32", accumulate=False) -> moe_linear_config:
+    return moe_linear_config(int(tokens), int(in_features), int(out_features),
+                             _index(ACTIVATIONS, activation, "activation"),
+                             _index(DTYPES, y_dtype, "y_dtype"),
+                             _index(DTYPES, dw_dtype, "dw_dtype"), int(bool(accumulate)))
+
+
+class moe_grouped_config(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("x_rows", ctypes.c_int64),
+                ("num_groups", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("out_features", ctypes.c_int32), ("row_div", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+def make_grouped_config(rows, num_groups, in_features, out_features, x_rows=None, row_div=1,
+                        y_dtype="bf16", dw_dtype="f32", accumulate=False) -> moe_grouped_config:
+    """x_rows: rows of x when row_ids is passed (default: rows)."""
+    return moe_grouped_config(int(rows), int(rows if x_rows is None else x_rows), int(num_groups),
+                              int(in_features), int(out_features), int(row_div),
+                              _index(DTYPES, y_dtype, "y_dtype"),
+                              _index(DTYPES, dw_dtype, "dw_dtype"), int(bool(accumulate)), 0)
+
+
+class moe_swiglu_config(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("inter", ctypes.c_int32), ("ld", ctypes.c_int32),
+                ("limit", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+def make_swiglu_config(rows, inter, ld=0, limit=0.0) -> moe_swiglu_config:
+    """ld: row stride of gate, up and their gradients (0: inter)."""
+    return moe_swiglu_config(int(rows), int(inter), int(ld), float(limit), 0)
+
+
 _lib = None
 
 
@@ -87,8 +139,22 @@ def load_library():
     lib.moe_dense_workspace_size.restype = sz
     lib.moe_dense_forward.argtypes = [dp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_forward_fused.argtypes = lib.moe_forward.argtypes
+    lp, gp, sp = (ctypes.POINTER(t) for t in (moe_linear_config, moe_grouped_config,
+                                              moe_swiglu_config))
+    lib.moe_linear_workspace_size.argtypes = [lp]
+    lib.moe_linear_workspace_size.restype = sz
+    lib.moe_linear_forward.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_linear_backward.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_grouped_workspace_size.argtypes = [gp]
+    lib.moe_grouped_workspace_size.restype = sz
+    lib.moe_grouped_forward.argtypes = [gp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_grouped_backward.argtypes = [gp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_swiglu_forward.argtypes = [sp, vp, vp, vp, vp]
+    lib.moe_swiglu_backward.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp]
     for f in ("moe_route", "moe_permute", "moe_forward", "moe_forward_timed",
-              "moe_workspace_view", "moe_dense_forward", "moe_forward_fp8", "moe_forward_fused"):
+              "moe_workspace_view", "moe_dense_forward", "moe_forward_fp8", "moe_forward_fused",
+              "moe_linear_forward", "moe_linear_backward", "moe_grouped_forward",
+              "moe_grouped_backward", "moe_swiglu_forward", "moe_swiglu_backward"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -97,7 +163,9 @@ def load_library():
 EXPORTED = ("moe_workspace_size", "moe_last_error", "moe_route", "moe_permute", "moe_forward",
             "moe_forward_timed", "moe_workspace_view", "moe_dense_workspace_size",
             "moe_dense_forward", "moe_forward_fp8", "moe_forward_fused",
-            "moe_forward_noalloc")
+            "moe_forward_noalloc", "moe_linear_workspace_size", "moe_linear_forward",
+            "moe_linear_backward", "moe_grouped_workspace_size", "moe_grouped_forward",
+            "moe_grouped_backward", "moe_swiglu_forward", "moe_swiglu_backward")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # MOE_NOALLOC_SCRATCH_BYTES
 
 
@@ -333,3 +401,149 @@ def moe_forward_fp8(cfg, x, router_w, router_bias, w8_gate, w8_up, w8_down, scal
         _ptr(y, _bf16(), "y", empty), _ptr(topk_ids_out, _i32(), "topk_ids_out", True),
         _ptr(topk_w_out, _f32(), "topk_w_out", True), _ptr(ws, None, "ws"),
         ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ------------------------------------------------------------------ linear and grouped products
+
+def _arg(t, name, dtypes, numel, optional=False):
+    """Device address of a contiguous tensor of `numel` elements on the current
+    device."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    p = _ptr(t, dtypes, name)
+    if t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+    _on_current_device(t, name)
+    return p
+
+
+def _on_current_device(t, name):
+    if t.get_device() != _torch().cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{_torch().cuda.current_device()}")
+
+
+def _of_dtype(index):
+    return _f32() if index == DTYPES.index("f32") else _bf16()
+
+
+def _workspace(ws):
+    """(address, bytes) of a workspace tensor."""
+    if ws is None:
+        raise ValueError("ws is required")
+    p = _ptr(ws, None, "ws")
+    _on_current_device(ws, "ws")
+    return p, ws.numel() * ws.element_size()
+
+
+def _alloc(nbytes, device):
+    torch = _torch()
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def moe_linear_workspace_size(cfg: moe_linear_config) -> int:
+    n = load_library().moe_linear_workspace_size(ctypes.byref(cfg))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, moe_last_error())
+    return int(n)
+
+
+def alloc_linear_workspace(cfg: moe_linear_config, device=None):
+    return _alloc(moe_linear_workspace_size(cfg), device)
+
+
+def moe_linear_forward(cfg, x, w, bias, residual, y, z=None, ws=None, stream=None):
+    """z = x W^T + bias; y = act(z) + residual (bias, residual, z: may be None)."""
+    T, K, F = cfg.tokens, cfg.in_features, cfg.out_features
+    bf = _bf16()
+    _check(load_library().moe_linear_forward(
+        ctypes.byref(cfg), _arg(x, "x", bf, T * K), _arg(w, "w", bf, F * K),
+        _arg(bias, "bias", _f32(), F, True), _arg(residual, "residual", bf, T * F, True),
+        _arg(y, "y", _of_dtype(cfg.y_dtype), T * F), _arg(z, "z", bf, T * F, True),
+        *_workspace(ws), _stream(stream)))
+
+
+def moe_linear_backward(cfg, dy, z, x, w, dz, dx, dw, dbias, ws=None, stream=None):
+    """dz, dx, dw and dbias of moe_linear_forward for dy; dx, dw and dbias may
+    be None, z and dz with activation "none"."""
+    T, K, F = cfg.tokens, cfg.in_features, cfg.out_features
+    bf = _bf16()
+    plain = cfg.activation == 0
+    _check(load_library().moe_linear_backward(
+        ctypes.byref(cfg), _arg(dy, "dy", bf, T * F), _arg(z, "z", bf, T * F, plain),
+        _arg(x, "x", bf, T * K, dw is None), _arg(w, "w", bf, F * K, dx is None),
+        _arg(dz, "dz", bf, T * F, plain), _arg(dx, "dx", bf, T * K, True),
+        _arg(dw, "dw", _of_dtype(cfg.dw_dtype), F * K, True),
+        _arg(dbias, "dbias", _f32(), F, True), *_workspace(ws), _stream(stream)))
+
+
+def moe_grouped_workspace_size(cfg: moe_grouped_config) -> int:
+    n = load_library().moe_grouped_workspace_size(ctypes.byref(cfg))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, moe_last_error())
+    return int(n)
+
+
+def alloc_grouped_workspace(cfg: moe_grouped_config, device=None):
+    return _alloc(moe_grouped_workspace_size(cfg), device)
+
+
+def moe_grouped_forward(cfg, x, row_ids, offsets, w, bias, y, ws=None, stream=None):
+    """y[r] = W_e x[src(r)] + bias_e for the rows r of each group e (row_ids
+    and bias: may be None)."""
+    P, E, K, F = cfg.rows, cfg.num_groups, cfg.in_features, cfg.out_features
+    bf, i32 = _bf16(), _i32()
+    _check(load_library().moe_grouped_forward(
+        ctypes.byref(cfg), _arg(x, "x", bf, cfg.x_rows * K),
+        _arg(row_ids, "row_ids", i32, P, True), _arg(offsets, "offsets", i32, E + 1),
+        _arg(w, "w", bf, E * F * K), _arg(bias, "bias", _f32(), E * F, True),
+        _arg(y, "y", _of_dtype(cfg.y_dtype), P * F), *_workspace(ws), _stream(stream)))
+
+
+def moe_grouped_backward(cfg, dy, x, row_ids, offsets, w, dx, dw, dbias, ws=None, stream=None):
+    """dx, dw and dbias of moe_grouped_forward for dy (each may be None)."""
+    P, E, K, F = cfg.rows, cfg.num_groups, cfg.in_features, cfg.out_features
+    bf, i32 = _bf16(), _i32()
+    _check(load_library().moe_grouped_backward(
+        ctypes.byref(cfg), _arg(dy, "dy", bf, P * F), _arg(x, "x", bf, cfg.x_rows * K, dw is None),
+        _arg(row_ids, "row_ids", i32, P, True), _arg(offsets, "offsets", i32, E + 1),
+        _arg(w, "w", bf, E * F * K, dx is None), _arg(dx, "dx", bf, P * K, True),
+        _arg(dw, "dw", _of_dtype(cfg.dw_dtype), E * F * K, True),
+        _arg(dbias, "dbias", _f32(), E * F, True), *_workspace(ws), _stream(stream)))
+
+
+def _rows_arg(t, name, cfg):
+    """Device address of a bf16 [rows][inter] tensor or view with the
+    configuration's row stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on the GPU, got {t.device}")
+    if t.dtype not in _bf16():
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_bf16()}")
+    if tuple(t.shape) != (cfg.rows, cfg.inter):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(cfg.rows, cfg.inter)}")
+    if t.stride(1) != 1 or (cfg.rows > 1 and t.stride(0) != (cfg.ld or cfg.inter)):
+        raise ValueError(f"{name} has strides {t.stride()}, expected ({cfg.ld or cfg.inter}, 1)")
+    _on_current_device(t, name)
+    return t.data_ptr()
+
+
+def moe_swiglu_forward(cfg, gate, up, h, stream=None):
+    """h = SiLU(min(gate, L)) * clamp(up, -L, L); gate and up may be the halves
+    of one [rows][2 inter] tensor (ld = 2 inter)."""
+    _check(load_library().moe_swiglu_forward(
+        ctypes.byref(cfg), _rows_arg(gate, "gate", cfg), _rows_arg(up, "up", cfg),
+        _arg(h, "h", _bf16(), cfg.rows * cfg.inter), _stream(stream)))
+
+
+def moe_swiglu_backward(cfg, dh, gate, up, dgate, dup, h=None, stream=None):
+    """dgate and dup for dh; h (may be None) is recomputed on the way."""
+    n = cfg.rows * cfg.inter
+    _check(load_library().moe_swiglu_backward(
+        ctypes.byref(cfg), _arg(dh, "dh", _bf16(), n), _rows_arg(gate, "gate", cfg),
+        _rows_arg(up, "up", cfg), _rows_arg(dgate, "dgate", cfg), _rows_arg(dup, "dup", cfg),
+        _arg(h, "h", _bf16(), n, True), _stream(stream)))

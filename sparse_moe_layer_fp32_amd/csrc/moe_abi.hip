@@ -7,12 +7,15 @@
 #include <mutex>
 #include <string>
 
+#include "abi_util.h"
 #include "kernels.h"
 #include "moe.h"
 
-namespace {
+namespace moe {
 
+namespace {
 thread_local std::string g_error;
+}  // namespace
 
 moe_status fail(moe_status st, const char* fmt, ...) {
   char buf[512];
@@ -29,8 +32,20 @@ moe_status ok() {
   return MOE_OK;
 }
 
-constexpr size_t kAlign = 256;
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+moe_status hip_fail(hipError_t e, const char* what) {
+  return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+}  // namespace moe
+
+namespace {
+
+using moe::align_up;
+using moe::aligned16;
+using moe::at;
+using moe::fail;
+using moe::hip_fail;
+using moe::ok;
 
 // Byte layout of the workspace for one configuration.
 struct Plan {
@@ -118,23 +133,6 @@ void make_plan(const moe_config* c, Plan* p) {
   p->o = take((P + (p->Is > 0 ? T64 : 0)) * p->H * 2);
   p->total = off;
 }
-
-bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-
-template <class T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
-}
-
-moe_status hip_fail(hipError_t e, const char* what) {
-  return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-#define MOE_CHECK_LAUNCH(expr, what)           \
-  do {                                         \
-    hipError_t e_ = (expr);                    \
-    if (e_ != hipSuccess) return hip_fail(e_, what); \
-  } while (0)
 
 moe_status check_ws(const Plan& p, const void* ws, size_t ws_bytes) {
   if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
@@ -505,7 +503,7 @@ size_t moe_workspace_size(const moe_config* cfg) {
   return p.total;
 }
 
-const char* moe_last_error(void) { return g_error.c_str(); }
+const char* moe_last_error(void) { return moe::g_error.c_str(); }
 
 moe_status moe_route(const moe_config* cfg, const uint16_t* x, const float* router_w,
                      const float* router_bias, int32_t* topk_ids, float* topk_w, void* ws,
