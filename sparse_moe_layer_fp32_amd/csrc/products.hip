@@ -1,29 +1,18 @@
 // Linear and grouped products on gfx950 matrix cores: y = x W^T with bias,
 // activation and residual, and the gradients dx = dy W and dW = dy^T x, for
-// one group of rows or for one group per expert with ragged sizes.
+// one group of rows or for one group per expert with ragged sizes.  The tile
+// itself (mainloop and epilogue) is in product_tile.h; this file finds each
+// block's tile, chooses tile shapes and joins split contractions.
 
 #include <algorithm>
 
-#include "activation.h"
-#include "products.h"
+#include "product_tile.h"
 
 namespace moe {
 
 namespace {
 
 constexpr int kGroupM = 8;  // row tiles walked together, so that they share column operands
-
-// The work of one block: a tile of one group's output and a contraction range.
-struct Unit {
-  int g;         // group
-  int row0;      // first output row (forward, input gradient: a row of all P;
-                 // weight gradient: an out feature)
-  int rows;      // output rows in the tile, >= 1
-  int col0;      // first output column
-  int begin;     // weight gradient: the group's first row and row count
-  int len;
-  int split;
-};
 
 __device__ __forceinline__ int clamp_row(int v, int64_t P) {
   return static_cast<int>(min<int64_t>(max(v, 0), P));
@@ -85,6 +74,7 @@ __device__ bool find_unit(const ProductArgs& p, int* sh, Unit* un) {
       if (w < wid) before += sh[w];
       total += sh[w];
     }
+    total = __builtin_amdgcn_readfirstlane(total);
     const int u = xcd_remap(blockIdx.x, total * NT * p.splits);
     if (u < 0) return false;
     int t = u % (total * NT) / NT;
@@ -105,10 +95,10 @@ __device__ bool find_unit(const ProductArgs& p, int* sh, Unit* un) {
       }
     }
     __syncthreads();
-    un->g = sh[16];
-    base = sh[17];
-    n = sh[18];
-    first_tile = sh[19];
+    un->g = __builtin_amdgcn_readfirstlane(sh[16]);
+    base = __builtin_amdgcn_readfirstlane(sh[17]);
+    n = __builtin_amdgcn_readfirstlane(sh[18]);
+    first_tile = __builtin_amdgcn_readfirstlane(sh[19]);
     __syncthreads();
   }
   if (!p.offsets) un->g = 0;
@@ -131,145 +121,19 @@ __device__ bool find_unit(const ProductArgs& p, int* sh, Unit* un) {
   return true;
 }
 
-// Bias, z, activation, residual and the store of eight consecutive columns.
-// Rounded once per output, from the fp32 sum.
-__device__ __forceinline__ void finish8(const ProductArgs& p, F8 v, const float* bias, int64_t row,
-                                        int col, int N) {
-  const int64_t at = row * N + col;
-  if (bias) {
-    const F8 b = load8(bias + col);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v.v[q] += b.v[q];
-  }
-  if (p.z) store8(p.z + at, v);
-  if (p.act != MOE_ACT_NONE)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v.v[q] = activate(v.v[q], p.act);
-  if (p.residual) {
-    const F8 r = load8(p.residual + at);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v.v[q] += r.v[q];
-  }
-  if (p.y_f32) {
-    float* y = static_cast<float*>(p.y) + at;
-    if (p.accumulate) {
-      const F8 o = load8(y);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v.v[q] += o.v[q];
-    }
-    store8(y, v);
-  } else {
-    uint16_t* y = static_cast<uint16_t*>(p.y) + at;
-    if (p.accumulate) {
-      const F8 o = load8(y);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v.v[q] += o.v[q];
-    }
-    store8(y, v);
-  }
-}
-
-// x's row of row r, or -1.
-__device__ __forceinline__ int64_t source_row(const ProductArgs& p, int r) {
-  if (!p.src) return r;
-  const int id = p.src[r];
-  if (id < 0) return -1;
-  const int64_t s = id / p.row_div;
-  return s < p.x_rows ? s : -1;
-}
-
-// The plainest tile: 64 x 64, staged through registers, both operands laid
-// down contraction-contiguous.
-template <int OP>
-__global__ __launch_bounds__(256) void product_simple(ProductArgs p) {
-  constexpr int BM = 64, BN = 64, BK = 32, LD = BK + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t as[BM * LD], bs[BN * LD];
-  __shared__ float out[BM * (BN + 4)];
-  __shared__ int sh[32];
+template <int OP, class T, bool GATHER>
+__global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::RING];
   Unit un;
-  if (!find_unit<OP, BM, BN, 256>(p, sh, &un)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-  const int N = OP == kForward ? p.F : p.K;
-  const int L = OP == kForward ? p.K : OP == kInputGrad ? p.F : un.len;
-  const int KT = (L + BK - 1) / BK, per = (KT + p.splits - 1) / p.splits;
-  const int k_first = min(KT, un.split * per), k_last = min(KT, k_first + per);
-  const uint16_t* w = p.b + (OP == kWeightGrad ? 0 : static_cast<int64_t>(un.g) * p.F * p.K);
-  f32x16 acc{};
-  float dbsum = 0.0f;
-  for (int kt = k_first; kt < k_last; ++kt) {
-    const int k0 = kt * BK;
-    u32x4 va{}, vb{};
-    {  // A: dy^T for the weight gradient, else rows of x or dy
-      if (OP == kWeightGrad) {
-        const int k = k0 + tid / 8, c = un.row0 + tid % 8 * 8;
-        if (k < L && c < p.F)
-          va = *reinterpret_cast<const u32x4*>(p.a + static_cast<int64_t>(un.begin + k) * p.F + c);
-      } else {
-        const int r = tid / 4, k = k0 + tid % 4 * 8;
-        if (r < un.rows && k < L) {
-          const int64_t s = OP == kForward ? source_row(p, un.row0 + r) : un.row0 + r;
-          if (s >= 0) va = *reinterpret_cast<const u32x4*>(p.a + s * L + k);
-        }
-      }
-      if (OP == kForward) {
-        const int r = un.col0 + tid / 4, k = k0 + tid % 4 * 8;
-        if (r < N && k < L) vb = *reinterpret_cast<const u32x4*>(w + static_cast<int64_t>(r) * L + k);
-      } else {
-        const int k = k0 + tid / 8, c = un.col0 + tid % 8 * 8;
-        if (k < L && c < N && (OP != kWeightGrad || p.y)) {
-          const int64_t s = OP == kWeightGrad ? source_row(p, un.begin + k) : k;
-          if (s >= 0) vb = *reinterpret_cast<const u32x4*>(w + s * N + c);
-        }
-      }
-    }
-    __syncthreads();
-    auto put = [&](uint16_t* lds, const u32x4& v, bool strided) {
-      if (!strided) {
-        *reinterpret_cast<u32x4*>(lds + tid / 4 * LD + tid % 4 * 8) = v;
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          lds[(tid % 8 * 8 + q) * LD + tid / 8] = static_cast<uint16_t>(v[q / 2] >> (q % 2 * 16));
-      }
-    };
-    put(as, va, OP == kWeightGrad);
-    put(bs, vb, OP != kForward);
-    __syncthreads();
-#pragma unroll
-    for (int ks = 0; ks < BK / 16; ++ks) {
-      const int o = 16 * ks + 8 * (lane >> 5);
-      const bf16x8 fa = *reinterpret_cast<const bf16x8*>(as + ((wid >> 1) * 32 + (lane & 31)) * LD + o);
-      const bf16x8 fb = *reinterpret_cast<const bf16x8*>(bs + ((wid & 1) * 32 + (lane & 31)) * LD + o);
-      acc = mfma32(fb, fa, acc);
-    }
-    if (OP == kWeightGrad && p.db && un.col0 == 0 && tid < BM)
-      for (int k = 0; k < BK; ++k) dbsum += bf16_to_f32(as[tid * LD + k]);
-  }
-#pragma unroll
-  for (int r = 0; r < 16; ++r)
-    out[((wid >> 1) * 32 + (lane & 31)) * (BN + 4) + (wid & 1) * 32 + mfma32_row(r, lane)] = acc[r];
-  __syncthreads();
-  for (int i = tid; i < BM * BN / 8; i += 256) {
-    const int r = i / (BN / 8), c = i % (BN / 8) * 8, col = un.col0 + c;
-    if (r >= un.rows || col >= N || (OP == kWeightGrad && !p.y)) continue;
-    F8 v;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) v.v[q] = out[r * (BN + 4) + c + q];
-    const int64_t row = (OP == kWeightGrad ? static_cast<int64_t>(un.g) * p.F : 0) + un.row0 + r;
-    if (p.splits > 1) {
-      const int64_t rows = OP == kWeightGrad ? static_cast<int64_t>(p.G) * p.F : p.P;
-      store8(p.part + (un.split * rows + row) * N + col, v);
-    } else {
-      finish8(p, v, p.bias ? p.bias + static_cast<int64_t>(un.g) * p.F : nullptr, row, col, N);
+  if (!find_unit<OP, T::BM, T::BN, T::THREADS>(p, reinterpret_cast<int*>(smem), &un)) return;
+  if constexpr (OP == kWeightGrad) {
+    if (p.accumulate && un.len == 0 && p.splits == 1) return;
+    if (p.db && un.col0 == 0) {
+      product_tile<OP, T, GATHER, true>(p, smem, un);
+      return;
     }
   }
-  if (OP == kWeightGrad && p.db && un.col0 == 0 && tid < un.rows) {
-    const int64_t i = static_cast<int64_t>(un.g) * p.F + un.row0 + tid;
-    if (p.splits > 1)
-      p.part_db[static_cast<int64_t>(un.split) * p.G * p.F + i] = dbsum;
-    else
-      p.db[i] = p.accumulate ? p.db[i] + dbsum : dbsum;
-  }
+  product_tile<OP, T, GATHER, false>(p, smem, un);
 }
 
 // Sums the contraction ranges' partial results in order and finishes them.
@@ -362,19 +226,50 @@ __global__ __launch_bounds__(256) void strip_sum_kernel(const float* __restrict_
   db[c] = accumulate ? db[c] + v : v;
 }
 
-template <int OP>
-hipError_t launch_op(const ProductArgs& p, hipStream_t stream) {
-  const int N = OP == kForward ? p.F : p.K;
-  const int64_t NT = (N + 63) / 64;
-  const int64_t tiles = OP == kWeightGrad ? static_cast<int64_t>(p.G) * ((p.F + 63) / 64)
-                        : p.offsets      ? p.P / 64 + std::min<int64_t>(p.G, p.P)
-                                         : (p.P + 63) / 64;
-  const int64_t units = tiles * NT * p.splits;
+// Tile shapes.
+enum Shape : int { kShapeBig, kShapeMid, kShapeFlat, kShapeSmall, kNumShapes };
+template <int OP> using Big = Tile<OP, 256, 256, 2, 4, 2, 3>;
+template <int OP> using Mid = Tile<OP, 128, 128, 2, 2, 2, 3>;
+template <int OP> using Flat = Tile<OP, 64, 256, 2, 4, 4, 4>;
+template <int OP> using Small = Tile<OP, 64, 64, 2, 2, 4, 4>;
+
+struct ShapeSize {
+  int bm, bn;
+};
+constexpr ShapeSize kShapeSizes[kNumShapes] = {{256, 256}, {128, 128}, {64, 256}, {64, 64}};
+
+// Tiles of a product, at most (the tiles of ragged groups are counted on the device).
+int64_t tile_count(int op, int64_t P, int G, int K, int F, bool grouped, ShapeSize s) {
+  const int64_t nt = ((op == kForward ? F : K) + s.bn - 1) / s.bn;
+  if (op == kWeightGrad) return static_cast<int64_t>(G) * ((F + s.bm - 1) / s.bm) * nt;
+  return (grouped ? P / s.bm + std::min<int64_t>(G, P) : (P + s.bm - 1) / s.bm) * nt;
+}
+
+template <int OP, class T>
+hipError_t launch_tiles(const ProductArgs& p, hipStream_t stream) {
+  const int64_t units =
+      tile_count(OP, p.P, p.G, OP == kWeightGrad && !p.y ? 1 : p.K, p.F, p.offsets != nullptr,
+                 {T::BM, T::BN}) * p.splits;
   if (units <= 0) return hipSuccess;
-  const int64_t grid = (units + kNumXcd - 1) / kNumXcd * kNumXcd;
-  product_simple<OP><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
-  hipError_t e = hipGetLastError();
+  const unsigned grid = static_cast<unsigned>((units + kNumXcd - 1) / kNumXcd * kNumXcd);
+  if (OP == kWeightGrad && p.src && p.y)
+    product_kernel<OP, T, OP == kWeightGrad><<<grid, T::THREADS, 0, stream>>>(p);
+  else
+    product_kernel<OP, T, false><<<grid, T::THREADS, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <int OP>
+hipError_t launch_op(const ProductArgs& p, int shape, hipStream_t stream) {
+  hipError_t e;
+  switch (shape) {
+    case kShapeBig: e = launch_tiles<OP, Big<OP>>(p, stream); break;
+    case kShapeMid: e = launch_tiles<OP, Mid<OP>>(p, stream); break;
+    case kShapeFlat: e = launch_tiles<OP, Flat<OP>>(p, stream); break;
+    default: e = launch_tiles<OP, Small<OP>>(p, stream); break;
+  }
   if (e != hipSuccess || p.splits == 1) return e;
+  const int N = OP == kForward ? p.F : p.K;
   const int64_t rows = OP == kWeightGrad ? static_cast<int64_t>(p.G) * p.F : p.P;
   const int64_t threads = rows * (N / 8) + (OP == kWeightGrad && p.db ? rows : 0);
   product_join<OP><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(p);
@@ -383,9 +278,44 @@ hipError_t launch_op(const ProductArgs& p, hipStream_t stream) {
 
 }  // namespace
 
+// Estimated microseconds of each shape: rounds of the GPU's tile slots times
+// contraction steps, each step costing more when a CU's second slot or all of
+// the GPU's memory paths are busy; a split adds the join and its traffic.
+struct ShapeCost {
+  int per_cu;          // tiles resident on a CU
+  float full, partly;  // us per step with all slots taken, with at most one tile per CU
+  float fixed;         // us per tile (start, first loads, epilogue)
+};
+constexpr ShapeCost kCosts[kNumShapes] = {
+    {1, 1.6f, 1.2f, 8.0f}, {2, 1.0f, 0.55f, 6.0f}, {1, 0.62f, 0.42f, 5.0f}, {2, 0.41f, 0.18f, 4.0f}};
+
 ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
-  (void)op, (void)P, (void)G, (void)K, (void)F, (void)cus;
-  return {0, 1};
+  const int64_t rows = op == kWeightGrad ? static_cast<int64_t>(G) * F : P;
+  const int64_t cols = op == kForward ? F : K;
+  const int64_t L = op == kForward ? K : op == kInputGrad ? F : (P + G - 1) / G;
+  const int64_t steps = std::max<int64_t>(1, (L + kStep - 1) / kStep);
+  ProductPlan best{kShapeSmall, 1};
+  float best_us = 0.0f;
+  for (int s = 0; s < kNumShapes; ++s) {
+    if (op == kWeightGrad && s == kShapeFlat) continue;
+    int64_t tiles = tile_count(op, P, G, K, F, false, kShapeSizes[s]);
+    if (op != kWeightGrad && G > 1)  // an expert with rows has half a tile too many
+      tiles += std::min<int64_t>(G, P) / 2 * ((cols + kShapeSizes[s].bn - 1) / kShapeSizes[s].bn);
+    for (int splits = 1; splits <= 16 && splits <= steps; splits *= 2) {
+      const ShapeCost& c = kCosts[s];
+      const int64_t units = tiles * splits, slots = static_cast<int64_t>(cus) * c.per_cu;
+      const int64_t rest = units % slots;
+      const float n = static_cast<float>((steps + splits - 1) / splits);
+      float us = static_cast<float>(units / slots) * (n * c.full + c.fixed);
+      if (rest) us += n * (rest <= cus ? c.partly : c.full) + c.fixed;
+      if (splits > 1) us += 5.0f + static_cast<float>(rows) * cols * 8.0f * splits / 3.5e6f;
+      if (best_us == 0.0f || us < best_us) {
+        best_us = us;
+        best = {s, splits};
+      }
+    }
+  }
+  return best;
 }
 
 size_t product_part_bytes(int op, int64_t P, int G, int K, int F, const ProductPlan& plan) {
@@ -399,10 +329,10 @@ hipError_t launch_product(int op, const ProductArgs& p, const ProductPlan& plan,
                           hipStream_t stream) {
   ProductArgs q = p;
   q.splits = plan.splits;
-  if (op == kForward) return launch_op<kForward>(q, stream);
-  if (op == kInputGrad) return launch_op<kInputGrad>(q, stream);
+  if (op == kForward) return launch_op<kForward>(q, plan.shape, stream);
+  if (op == kInputGrad) return launch_op<kInputGrad>(q, plan.shape, stream);
   q.part_db = q.part + static_cast<int64_t>(q.splits) * q.G * q.F * q.K;
-  return launch_op<kWeightGrad>(q, stream);
+  return launch_op<kWeightGrad>(q, plan.shape, stream);
 }
 
 hipError_t launch_source_rows(const int32_t* row_ids, int row_div, int64_t x_rows, int64_t P,
