@@ -405,37 +405,79 @@ def moe_forward_fp8(cfg, x, router_w, router_bias, w8_gate, w8_up, w8_down, scal
 
 # ------------------------------------------------------------------ linear and grouped products
 
-def _arg(t, name, dtypes, numel, optional=False):
-    """Device address of a contiguous tensor of `numel` elements on the current
-    device."""
-    if t is None:
-        if optional:
+class _Args:
+    """Checks of one call's tensors, in the order cheapest for tensors that
+    pass (a call of a few microseconds of GPU work spends as long here
+    otherwise), and the errors for those that do not."""
+    __slots__ = ("device", "torch", "bf16", "f32", "i32")
+
+    def __init__(self):
+        torch = _torch()
+        self.torch = torch
+        # -2: no tensor's device (a host tensor's is -1)
+        self.device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+        self.bf16 = (torch.bfloat16, torch.uint16, torch.int16)
+        self.f32 = (torch.float32,)
+        self.i32 = (torch.int32,)
+
+    def __call__(self, t, name, dtypes, numel, optional=False):
+        """Device address of a contiguous tensor of `numel` elements on the
+        current device."""
+        if t is None and optional:
             return None
-        raise ValueError(f"{name} is required")
-    p = _ptr(t, dtypes, name)
-    if t.numel() != numel:
-        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-    _on_current_device(t, name)
-    return p
+        if (isinstance(t, self.torch.Tensor) and t.dtype in dtypes and t.numel() == numel
+                and t.is_contiguous() and t.get_device() == self.device):
+            return t.data_ptr()
+        _ptr(t, dtypes, name)
+        if t.numel() != numel:
+            raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+        return self._elsewhere(t, name)
 
+    def rows(self, t, name, cfg):
+        """Device address of a bf16 [rows][inter] tensor or view with the
+        configuration's row stride."""
+        ld = cfg.ld or cfg.inter
+        if (isinstance(t, self.torch.Tensor) and t.dtype in self.bf16
+                and t.get_device() == self.device and t.shape == (cfg.rows, cfg.inter)
+                and (t.stride() == (ld, 1) or cfg.rows == 1 and t.stride(1) == 1)):
+            return t.data_ptr()
+        if not isinstance(t, self.torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be on the GPU, got {t.device}")
+        if t.dtype not in self.bf16:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected one of {self.bf16}")
+        if t.shape != (cfg.rows, cfg.inter):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(cfg.rows, cfg.inter)}")
+        if t.stride(1) != 1 or (cfg.rows > 1 and t.stride(0) != ld):
+            raise ValueError(f"{name} has strides {t.stride()}, expected ({ld}, 1)")
+        return self._elsewhere(t, name)
 
-def _on_current_device(t, name):
-    if t.get_device() != _torch().cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{_torch().cuda.current_device()}")
+    def of(self, dtype):
+        """Tensor types of a MOE_DTYPE_*."""
+        return self.f32 if dtype == 1 else self.bf16
 
+    def workspace(self, ws):
+        """(address, bytes) of a workspace tensor."""
+        if ws is None:
+            raise ValueError("ws is required")
+        n = ws.numel() if isinstance(ws, self.torch.Tensor) else 0
+        return self(ws, "ws", (getattr(ws, "dtype", None),), n), n * ws.element_size()
 
-def _of_dtype(index):
-    return _f32() if index == DTYPES.index("f32") else _bf16()
+    def stream(self, stream):
+        """The HIP stream: `stream`, or torch's current one (by its raw handle
+        where torch gives it: a Stream object costs 2.5 us)."""
+        if stream is None:
+            raw = getattr(self.torch._C, "_cuda_getCurrentRawStream", None)
+            if raw is not None and self.device >= 0:
+                return raw(self.device)
+        return _stream(stream)
 
-
-def _workspace(ws):
-    """(address, bytes) of a workspace tensor."""
-    if ws is None:
-        raise ValueError("ws is required")
-    p = _ptr(ws, None, "ws")
-    _on_current_device(ws, "ws")
-    return p, ws.numel() * ws.element_size()
+    def _elsewhere(self, t, name):
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} is on {t.device}, the current device is "
+                             f"cuda:{self.device}")
+        return t.data_ptr()
 
 
 def _alloc(nbytes, device):
@@ -457,26 +499,28 @@ def alloc_linear_workspace(cfg: moe_linear_config, device=None):
 def moe_linear_forward(cfg, x, w, bias, residual, y, z=None, ws=None, stream=None):
     """z = x W^T + bias; y = act(z) + residual (bias, residual, z: may be None)."""
     T, K, F = cfg.tokens, cfg.in_features, cfg.out_features
-    bf = _bf16()
+    a = _Args()
+    bf = a.bf16
     _check(load_library().moe_linear_forward(
-        ctypes.byref(cfg), _arg(x, "x", bf, T * K), _arg(w, "w", bf, F * K),
-        _arg(bias, "bias", _f32(), F, True), _arg(residual, "residual", bf, T * F, True),
-        _arg(y, "y", _of_dtype(cfg.y_dtype), T * F), _arg(z, "z", bf, T * F, True),
-        *_workspace(ws), _stream(stream)))
+        ctypes.byref(cfg), a(x, "x", bf, T * K), a(w, "w", bf, F * K),
+        a(bias, "bias", a.f32, F, True), a(residual, "residual", bf, T * F, True),
+        a(y, "y", a.of(cfg.y_dtype), T * F), a(z, "z", bf, T * F, True),
+        *a.workspace(ws), a.stream(stream)))
 
 
 def moe_linear_backward(cfg, dy, z, x, w, dz, dx, dw, dbias, ws=None, stream=None):
     """dz, dx, dw and dbias of moe_linear_forward for dy; dx, dw and dbias may
     be None, z and dz with activation "none"."""
     T, K, F = cfg.tokens, cfg.in_features, cfg.out_features
-    bf = _bf16()
+    a = _Args()
+    bf = a.bf16
     plain = cfg.activation == 0
     _check(load_library().moe_linear_backward(
-        ctypes.byref(cfg), _arg(dy, "dy", bf, T * F), _arg(z, "z", bf, T * F, plain),
-        _arg(x, "x", bf, T * K, dw is None), _arg(w, "w", bf, F * K, dx is None),
-        _arg(dz, "dz", bf, T * F, plain), _arg(dx, "dx", bf, T * K, True),
-        _arg(dw, "dw", _of_dtype(cfg.dw_dtype), F * K, True),
-        _arg(dbias, "dbias", _f32(), F, True), *_workspace(ws), _stream(stream)))
+        ctypes.byref(cfg), a(dy, "dy", bf, T * F), a(z, "z", bf, T * F, plain),
+        a(x, "x", bf, T * K, dw is None), a(w, "w", bf, F * K, dx is None),
+        a(dz, "dz", bf, T * F, plain), a(dx, "dx", bf, T * K, True),
+        a(dw, "dw", a.of(cfg.dw_dtype), F * K, True), a(dbias, "dbias", a.f32, F, True),
+        *a.workspace(ws), a.stream(stream)))
 
 
 def moe_grouped_workspace_size(cfg: moe_grouped_config) -> int:
@@ -494,56 +538,42 @@ def moe_grouped_forward(cfg, x, row_ids, offsets, w, bias, y, ws=None, stream=No
     """y[r] = W_e x[src(r)] + bias_e for the rows r of each group e (row_ids
     and bias: may be None)."""
     P, E, K, F = cfg.rows, cfg.num_groups, cfg.in_features, cfg.out_features
-    bf, i32 = _bf16(), _i32()
+    a = _Args()
+    bf = a.bf16
     _check(load_library().moe_grouped_forward(
-        ctypes.byref(cfg), _arg(x, "x", bf, cfg.x_rows * K),
-        _arg(row_ids, "row_ids", i32, P, True), _arg(offsets, "offsets", i32, E + 1),
-        _arg(w, "w", bf, E * F * K), _arg(bias, "bias", _f32(), E * F, True),
-        _arg(y, "y", _of_dtype(cfg.y_dtype), P * F), *_workspace(ws), _stream(stream)))
+        ctypes.byref(cfg), a(x, "x", bf, cfg.x_rows * K), a(row_ids, "row_ids", a.i32, P, True),
+        a(offsets, "offsets", a.i32, E + 1), a(w, "w", bf, E * F * K),
+        a(bias, "bias", a.f32, E * F, True), a(y, "y", a.of(cfg.y_dtype), P * F),
+        *a.workspace(ws), a.stream(stream)))
 
 
 def moe_grouped_backward(cfg, dy, x, row_ids, offsets, w, dx, dw, dbias, ws=None, stream=None):
     """dx, dw and dbias of moe_grouped_forward for dy (each may be None)."""
     P, E, K, F = cfg.rows, cfg.num_groups, cfg.in_features, cfg.out_features
-    bf, i32 = _bf16(), _i32()
+    a = _Args()
+    bf = a.bf16
     _check(load_library().moe_grouped_backward(
-        ctypes.byref(cfg), _arg(dy, "dy", bf, P * F), _arg(x, "x", bf, cfg.x_rows * K, dw is None),
-        _arg(row_ids, "row_ids", i32, P, True), _arg(offsets, "offsets", i32, E + 1),
-        _arg(w, "w", bf, E * F * K, dx is None), _arg(dx, "dx", bf, P * K, True),
-        _arg(dw, "dw", _of_dtype(cfg.dw_dtype), E * F * K, True),
-        _arg(dbias, "dbias", _f32(), E * F, True), *_workspace(ws), _stream(stream)))
-
-
-def _rows_arg(t, name, cfg):
-    """Device address of a bf16 [rows][inter] tensor or view with the
-    configuration's row stride."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be on the GPU, got {t.device}")
-    if t.dtype not in _bf16():
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_bf16()}")
-    if tuple(t.shape) != (cfg.rows, cfg.inter):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(cfg.rows, cfg.inter)}")
-    if t.stride(1) != 1 or (cfg.rows > 1 and t.stride(0) != (cfg.ld or cfg.inter)):
-        raise ValueError(f"{name} has strides {t.stride()}, expected ({cfg.ld or cfg.inter}, 1)")
-    _on_current_device(t, name)
-    return t.data_ptr()
+        ctypes.byref(cfg), a(dy, "dy", bf, P * F), a(x, "x", bf, cfg.x_rows * K, dw is None),
+        a(row_ids, "row_ids", a.i32, P, True), a(offsets, "offsets", a.i32, E + 1),
+        a(w, "w", bf, E * F * K, dx is None), a(dx, "dx", bf, P * K, True),
+        a(dw, "dw", a.of(cfg.dw_dtype), E * F * K, True), a(dbias, "dbias", a.f32, E * F, True),
+        *a.workspace(ws), a.stream(stream)))
 
 
 def moe_swiglu_forward(cfg, gate, up, h, stream=None):
     """h = SiLU(min(gate, L)) * clamp(up, -L, L); gate and up may be the halves
     of one [rows][2 inter] tensor (ld = 2 inter)."""
+    a = _Args()
     _check(load_library().moe_swiglu_forward(
-        ctypes.byref(cfg), _rows_arg(gate, "gate", cfg), _rows_arg(up, "up", cfg),
-        _arg(h, "h", _bf16(), cfg.rows * cfg.inter), _stream(stream)))
+        ctypes.byref(cfg), a.rows(gate, "gate", cfg), a.rows(up, "up", cfg),
+        a(h, "h", a.bf16, cfg.rows * cfg.inter), a.stream(stream)))
 
 
 def moe_swiglu_backward(cfg, dh, gate, up, dgate, dup, h=None, stream=None):
     """dgate and dup for dh; h (may be None) is recomputed on the way."""
     n = cfg.rows * cfg.inter
+    a = _Args()
     _check(load_library().moe_swiglu_backward(
-        ctypes.byref(cfg), _arg(dh, "dh", _bf16(), n), _rows_arg(gate, "gate", cfg),
-        _rows_arg(up, "up", cfg), _rows_arg(dgate, "dgate", cfg), _rows_arg(dup, "dup", cfg),
-        _arg(h, "h", _bf16(), n, True), _stream(stream)))
+        ctypes.byref(cfg), a(dh, "dh", a.bf16, n), a.rows(gate, "gate", cfg),
+        a.rows(up, "up", cfg), a.rows(dgate, "dgate", cfg), a.rows(dup, "dup", cfg),
+        a(h, "h", a.bf16, n, True), a.stream(stream)))

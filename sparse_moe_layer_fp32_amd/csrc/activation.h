@@ -116,6 +116,14 @@ __device__ __forceinline__ void store8(float* p, const F8& f) {
   reinterpret_cast<f32x4*>(p)[0] = f32x4{f.v[0], f.v[1], f.v[2], f.v[3]};
   reinterpret_cast<f32x4*>(p)[1] = f32x4{f.v[4], f.v[5], f.v[6], f.v[7]};
 }
+__device__ __forceinline__ void stream8(float* p, const F8& f) {
+  __builtin_nontemporal_store(f32x4{f.v[0], f.v[1], f.v[2], f.v[3]}, reinterpret_cast<f32x4*>(p));
+  __builtin_nontemporal_store(f32x4{f.v[4], f.v[5], f.v[6], f.v[7]},
+                              reinterpret_cast<f32x4*>(p) + 1);
+}
+__device__ __forceinline__ void stream8(uint16_t* p, const F8& f) {
+  __builtin_nontemporal_store(pack8(f), reinterpret_cast<u32x4*>(p));
+}
 
 }  // namespace
 

@@ -2,16 +2,16 @@
 // forward product y = x W^T, the input gradient dx = dy W and the weight
 // gradient dW = dy^T x share this mainloop.
 //
-//  * bf16 x bf16 -> fp32 on v_mfma_f32_32x32x16_bf16, contraction steps of 64.
+//  * bf16 x bf16 -> fp32 on v_mfma_f32_32x32x16_bf16, contraction steps of 64 (or 32).
 //  * An operand whose contraction runs along its rows in memory (x and W of
 //    the forward product, dy of the input gradient) is laid down in LDS as
-//    [tile row][64], 128-byte rows, and a fragment is one 16-byte read.  An
+//    [tile row][step], and a fragment is one 16-byte read.  An
 //    operand whose contraction runs across rows (W of the input gradient,
-//    both of the weight gradient) is laid down as it lies in memory, [64][tile
+//    both of the weight gradient) is laid down as it lies in memory, [step][tile
 //    column], and a fragment is two transposing reads (ds_read_b64_tr_b16: the
 //    16 lanes of a group read four rows of 16 columns and each gets one
 //    column's four values), so no operand is transposed in memory.
-//  * 16-byte chunks are XOR-swizzled: contiguous rows by (row >> 1) & 7,
+//  * 16-byte chunks are XOR-swizzled: 128-byte rows by (row >> 1) & 7,
 //    strided rows by 4 (row & 3) (the four rows a lane group reads land in
 //    different 64-byte quarters of the banks).
 //  * Panels go memory -> LDS with buffer_load ... lds.  A lane whose row or
@@ -34,12 +34,14 @@ namespace moe {
 
 namespace {
 
+// The tile's lambdas hold its accumulators by reference: one that is called
+// rather than inlined would put them in memory.
+#define MOE_INLINE __attribute__((always_inline))
+
 typedef __attribute__((address_space(3))) void lds_void;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-typedef const __attribute__((address_space(4))) int const_int;
 
-constexpr int kStep = 64;                     // contraction values per stage
 // Buffers are described with kRecords bytes whatever they hold: what keeps a
 // lane inside its operand is its offset, kOutside where it has nothing to read.
 constexpr uint32_t kRecords = 0xF0000000u;
@@ -63,42 +65,58 @@ struct Unit {
   int split;
 };
 
-// Bias, z, activation, residual and the store of eight consecutive columns.
-// Rounded once per output, from the fp32 sum.
-__device__ __forceinline__ void finish8(const ProductArgs& p, F8 v, const float* bias, int64_t row,
-                                        int col, int N) {
-  const int64_t at = row * N + col;
-  if (bias) {
-    const F8 b = load8(bias + col);
+// Bias, z, activation, residual and the store of eight consecutive columns at
+// element `at` of the output, rounded once per output from the fp32 sum.
+// bias and res are zeros where there is none; ACT: the activation, or -1 for
+// p.act.
+template <int ACT>
+__device__ __forceinline__ void finish8(const ProductArgs& p, F8 v, const F8& bias, const F8& res,
+                                        int64_t at) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v.v[q] += b.v[q];
-  }
+  for (int q = 0; q < 8; ++q) v.v[q] += bias.v[q];
   if (p.z) store8(p.z + at, v);
-  if (p.act != MOE_ACT_NONE)
+  const int act = ACT < 0 ? p.act : ACT;
+  if (act != MOE_ACT_NONE)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v.v[q] = activate(v.v[q], p.act);
-  if (p.residual) {
-    const F8 r = load8(p.residual + at);
+    for (int q = 0; q < 8; ++q) v.v[q] = activate(v.v[q], act);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v.v[q] += r.v[q];
+  for (int q = 0; q < 8; ++q) v.v[q] += res.v[q];
+  if (p.y_f32)
+    store8(static_cast<float*>(p.y) + at, v);
+  else
+    store8(static_cast<uint16_t*>(p.y) + at, v);
+}
+
+// The same for one piece on its own.
+__device__ __forceinline__ void finish_one(const ProductArgs& p, const F8& v, const float* bias,
+                                           int64_t row, int col, int N) {
+  const int64_t at = row * N + col;
+  const F8 b = bias ? load8(bias + col) : F8{};
+  const F8 r = p.residual ? load8(p.residual + at) : F8{};
+  finish8<-1>(p, v, b, r, at);
+}
+
+// A gradient's eight consecutive columns: stored, or added to what is there.
+// STREAM: with the non-temporal hint (a constant, as stores that differ in the
+// hint alone are merged without it).
+template <bool STREAM, class E>
+__device__ __forceinline__ void put_grad8(E* y, F8 v, bool accumulate) {
+  if (accumulate) {
+    const F8 o = load8(y);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v.v[q] += o.v[q];
   }
-  if (p.y_f32) {
-    float* y = static_cast<float*>(p.y) + at;
-    if (p.accumulate) {
-      const F8 o = load8(y);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v.v[q] += o.v[q];
-    }
+  if (STREAM)
+    stream8(y, v);
+  else
     store8(y, v);
-  } else {
-    uint16_t* y = static_cast<uint16_t*>(p.y) + at;
-    if (p.accumulate) {
-      const F8 o = load8(y);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v.v[q] += o.v[q];
-    }
-    store8(y, v);
-  }
+}
+template <bool STREAM>
+__device__ __forceinline__ void put_grad8(const ProductArgs& p, const F8& v, int64_t at) {
+  if (p.y_f32)
+    put_grad8<STREAM>(static_cast<float*>(p.y) + at, v, p.accumulate);
+  else
+    put_grad8<STREAM>(static_cast<uint16_t*>(p.y) + at, v, p.accumulate);
 }
 
 // x's row of row r, or -1.
@@ -118,20 +136,22 @@ __device__ __forceinline__ s16x4 read_transposed(lds_s16x4* __restrict__ at) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(at);
 }
 
-// A panel of D tile rows (or columns) by kStep contraction values in LDS,
-// filled by pieces of 1 KiB (one wave instruction each).
-template <int D, bool STRIDED>
+// A panel of D tile rows (or columns) by BK contraction values in LDS, filled
+// by pieces of 1 KiB (one wave instruction each).
+template <int D, int BK, bool STRIDED>
 struct Panel {
-  static constexpr int BYTES = D * kStep * 2;
+  static constexpr int BYTES = D * BK * 2;
   static constexpr int PIECES = BYTES / 1024;
-  static constexpr int CPR = STRIDED ? D / 8 : 8;  // 16-byte chunks per LDS row
-  static constexpr int RPP = 64 / CPR;             // LDS rows per piece
+  static constexpr int CPR = STRIDED ? D / 8 : BK / 8;  // 16-byte chunks per LDS row
+  static constexpr int RPP = 64 / CPR;                  // LDS rows per piece
+  static_assert(BK == 64 || BK == 32, "contraction step");
   static __device__ __forceinline__ int swz(int row) {
-    return !STRIDED ? (row >> 1) & 7 : D >= 128 ? 4 * (row & 3) : 4 * ((row >> 1) & 1);
+    if (!STRIDED) return BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3;
+    return D >= 128 ? 4 * (row & 3) : 4 * ((row >> 1) & 1);
   }
   // Fragment base address of this lane for the 32 rows (columns) from `first`.
   static __device__ __forceinline__ int frag_base(int first, int lane) {
-    if (!STRIDED) return (first + (lane & 31)) * 128;
+    if (!STRIDED) return (first + (lane & 31)) * BK * 2;
     // row 8 (lane / 32) + (lane % 16) / 4, columns first + 16 ((lane / 16) % 2) + 4 (lane % 4)
     const int row = 8 * (lane >> 5) + ((lane & 15) >> 2);
     const int chunk = first / 8 + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
@@ -140,7 +160,7 @@ struct Panel {
   // The 8 contraction values 16 ks + 8 (lane / 32) .. of the lane's row.
   static __device__ __forceinline__ bf16x8 frag(uint8_t* panel, int base, int ks, int lane) {
     if constexpr (!STRIDED) {
-      const int sw = ((2 * ks + (lane >> 5)) ^ (((lane & 31) >> 1) & 7)) * 16;
+      const int sw = ((2 * ks + (lane >> 5)) ^ swz(lane & 31)) * 16;
       return *reinterpret_cast<const bf16x8*>(panel + base + sw);
     } else {
       // rows 4 apart share row & 3 (and, D = 64, differ in (row >> 1) & 1 by none)
@@ -153,15 +173,15 @@ struct Panel {
   }
 };
 
-template <int OP, int BM_, int BN_, int WM_, int WN_, int SA_, int SB_>
+template <int OP, int BM_, int BN_, int WM_, int WN_, int SA_, int SB_, int BK_ = 64>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, SA = SA_, SB = SB_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, SA = SA_, SB = SB_, BK = BK_;
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr int MB = BM / WM / 32, NB = BN / WN / 32;  // 32 x 32 blocks per wave
-  using PA = Panel<BM, OP == kWeightGrad>;
-  using PB = Panel<BN, OP != kForward>;
+  using PA = Panel<BM, BK, OP == kWeightGrad>;
+  using PB = Panel<BN, BK, OP != kForward>;
   static constexpr int JA = PA::PIECES / NW, JB = PB::PIECES / NW;  // pieces per wave and stage
-  static constexpr int KS = kStep / 16;
+  static constexpr int KS = BK / 16;
   static constexpr int RING = SA * PA::BYTES + SB * PB::BYTES;
   // the fp32 tile leaves in passes that fit the ring
   static constexpr int PASSES = (BM * BN * 4 + RING - 1) / RING;
@@ -179,6 +199,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
   using PB = typename T::PB;
   const int N = OP == kForward ? p.F : p.K;
   const int L = OP == kForward ? p.K : OP == kInputGrad ? p.F : un.len;
+  constexpr int kStep = T::BK;
   const int KT = (L + kStep - 1) / kStep;
   const int per = (KT + p.splits - 1) / p.splits;
   const int k_first = min(KT, un.split * per), k_last = min(KT, k_first + per);
@@ -252,39 +273,42 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
   }
   uint8_t* const aring = smem;
   uint8_t* const bring = smem + T::SA * PA::BYTES;
-  auto load = [&](const char* base, int64_t step, int kt, uint32_t off, uint8_t* lds) {
+  auto load = [&](const char* base, int64_t step, int kt, uint32_t off, uint8_t* lds) MOE_INLINE {
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char*>(base + kt * step), 0, static_cast<int>(kRecords), 0x00027000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, 0, 0, 0);
   };
-  auto issue_a = [&](int kt, int j) {
+  auto issue_a = [&](int kt, int j) MOE_INLINE {
     const uint32_t off = (kt == KT - 1 && atail[j]) ? kOutside : aoff[j];
     load(abase, astep, kt, off,
          aring + ((kt - k_first) % T::SA) * PA::BYTES + (wid * T::JA + j) * 1024);
   };
-  // Gathered rows of the weight gradient: the wave's rows of a stage are
-  // consecutive, so their sources come by scalar loads, a stage ahead.
-  constexpr int IDS = GATHER ? PB::RPP * T::JB : 1;
-  int ids[IDS];
-  auto fetch_ids = [&](int kt) {
+  // Gathered rows of the weight gradient: each lane loads the sources of its
+  // rows of a stage one step before the stage is requested and ahead of that
+  // step's other loads, so that the ring's own wait covers them.
+  int ids[T::JB], ids_now[T::JB];
+  auto use_ids = [&]() MOE_INLINE {
+    if constexpr (GATHER)
+#pragma unroll
+      for (int j = 0; j < T::JB; ++j) ids_now[j] = ids[j];
+  };
+  auto fetch_ids = [&](int kt) MOE_INLINE {
     if constexpr (GATHER) {
       if (kt < k_last) {
-        const const_int* s = (const const_int*)(p.src + un.begin + kt * kStep + wid * IDS);
+        const int32_t* s = p.src + un.begin + kt * kStep;  // into the padding at most
 #pragma unroll
-        for (int i = 0; i < IDS; ++i) {
-          const int id = s[i];  // in the padding behind the last row at most
-          ids[i] = kt * kStep + wid * IDS + i < L ? id : -1;
-        }
+        for (int j = 0; j < T::JB; ++j)
+          ids[j] = s[PB::RPP * (wid * T::JB + j) + lane / PB::CPR];
       }
     }
   };
-  auto issue_b = [&](int kt, int j) {
+  auto issue_b = [&](int kt, int j) MOE_INLINE {
     uint32_t off = boff[j];
     if constexpr (GATHER) {
-      int s = ids[PB::RPP * j];
-#pragma unroll
-      for (int i = 1; i < PB::RPP; ++i) s = lane / PB::CPR == i ? ids[PB::RPP * j + i] : s;
-      off = s < 0 || off == kOutside ? kOutside : off + static_cast<uint32_t>(s) * p.K * 2;
+      const int s = ids_now[j];
+      off = s < 0 || off == kOutside || (kt == KT - 1 && btail[j])
+                ? kOutside
+                : off + static_cast<uint32_t>(s) * p.K * 2;
     } else {
       off = (kt == KT - 1 && btail[j]) ? kOutside : off;
     }
@@ -305,12 +329,22 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
   for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
-  f32x16 dbacc{};
+  // db: the wave's blocks of out features are wn, wn + WN, ..
+  constexpr int DBN = (T::MB + T::WN - 1) / T::WN;
+  f32x16 dbacc[DBN];
+  // (read on its own: chosen among the wave's fragments, the compiler would
+  // index them in scratch memory)
+  int dbbase[DBN];
+#pragma unroll
+  for (int i = 0; i < DBN; ++i) {
+    dbacc[i] = f32x16{};
+    dbbase[i] = PA::frag_base(wm * (T::BM / T::WM) + 32 * ((wn + i * T::WN) % T::MB), lane);
+  }
   const __bf16 one = static_cast<__bf16>(1.0f);
   const bf16x8 ones{one, one, one, one, one, one, one, one};
 
   bf16x8 af[2][T::MB], bf[2][T::NB];
-  auto load_frags = [&](int kt, int ks, int set) {
+  auto load_frags = [&](int kt, int ks, int set) MOE_INLINE {
     uint8_t* sa = aring + ((kt - k_first) % T::SA) * PA::BYTES;
     uint8_t* sb = bring + ((kt - k_first) % T::SB) * PB::BYTES;
 #pragma unroll
@@ -325,7 +359,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
   // flight.  Equal rings: both are requested S - 1 steps ahead.
   constexpr bool SPLIT = T::SA != T::SB;
   constexpr int REFILLS = SPLIT ? T::JB : T::JA + T::JB;
-  auto refill = [&](int kt, int d) {
+  auto refill = [&](int kt, int d) MOE_INLINE {
     if (SPLIT)
       issue_b(kt + T::SB - 1, d);
     else if (d < T::JA)
@@ -333,7 +367,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
     else
       issue_b(kt + T::SB - 1, d - T::JA);
   };
-  auto step_end = [&](int kt) {
+  auto step_end = [&](int kt) MOE_INLINE {
     if (kt + T::SB - 1 < k_last)
       wait_loads<(SPLIT ? T::JB : (T::SB - 2) * (T::JA + T::JB))>();
     else
@@ -345,13 +379,14 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
     for (int s = 0; s < T::SB - 1; ++s)
       if (k_first + s < k_last) {
         fetch_ids(k_first + s);
+        use_ids();
         if (s < T::SA - 1)
 #pragma unroll
           for (int j = 0; j < T::JA; ++j) issue_a(k_first + s, j);
 #pragma unroll
         for (int j = 0; j < T::JB; ++j) issue_b(k_first + s, j);
       }
-    fetch_ids(k_first + T::SB - 1);
+    fetch_ids(k_first + T::SB - 1);  // for the first step's refill
     if (k_first + T::SB - 2 < k_last)
       wait_loads<(T::SB - 2) * (SPLIT ? T::JB : T::JA + T::JB)>();
     else
@@ -362,18 +397,23 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
     const bool has_work = wm * (T::BM / T::WM) < un.rows && wn * (T::BN / T::WN) < cols;
     if (!has_work && !DB) {
       for (int kt = k_first; kt < k_last; ++kt) {
+        use_ids();
+        fetch_ids(kt + T::SB);
         if (SPLIT && kt + 1 < k_last)
 #pragma unroll
           for (int j = 0; j < T::JA; ++j) issue_a(kt + 1, j);
         if (kt + T::SB - 1 < k_last)
 #pragma unroll
           for (int d = 0; d < REFILLS; ++d) refill(kt, d);
-        fetch_ids(kt + T::SB);
         if (kt + 1 < k_last) step_end(kt);
       }
     } else {
-      auto step = [&](int kt, auto REFILL) {
+      auto step = [&](int kt, auto REFILL) MOE_INLINE {
         constexpr bool more = decltype(REFILL)::value;
+        if (more) {
+          use_ids();
+          fetch_ids(kt + T::SB);
+        }
         if (SPLIT && kt + 1 < k_last)
 #pragma unroll
           for (int j = 0; j < T::JA; ++j) issue_a(kt + 1, j);
@@ -381,12 +421,13 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
 #pragma unroll
         for (int ks = 0; ks < T::KS; ++ks) {
           if (ks + 1 < T::KS) load_frags(kt, ks + 1, (ks + 1) & 1);
-          if constexpr (DB) {
-            bf16x8 mine = af[ks & 1][0];
+          if constexpr (DB)
 #pragma unroll
-            for (int mb = 1; mb < T::MB; ++mb) mine = wn == mb ? af[ks & 1][mb] : mine;
-            dbacc = mfma32(ones, mine, dbacc);
-          }
+            for (int i = 0; i < DBN; ++i)
+              dbacc[i] = mfma32(ones,
+                                PA::frag(aring + ((kt - k_first) % T::SA) * PA::BYTES, dbbase[i],
+                                         ks, lane),
+                                dbacc[i]);
 #pragma unroll
           for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
@@ -400,7 +441,6 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
         if (more && MFMAS / EVERY < REFILLS)
 #pragma unroll
           for (int d = MFMAS / EVERY; d < REFILLS; ++d) refill(kt, d);
-        if (more) fetch_ids(kt + T::SB);
         if (kt + 1 < k_last) step_end(kt);
       };
       int kt = k_first;
@@ -414,24 +454,38 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
   const int64_t out_row0 = (OP == kWeightGrad ? static_cast<int64_t>(un.g) * p.F : 0) + un.row0;
   const int64_t out_rows = OP == kWeightGrad ? static_cast<int64_t>(p.G) * p.F : p.P;
   if constexpr (DB) {
-    const int r = wm * (T::BM / T::WM) + 32 * wn + (lane & 31);
-    if (wn < T::MB && lane < 32 && r < un.rows) {
-      const int64_t i = out_row0 + r;
-      if (p.splits > 1)
-        p.part_db[un.split * out_rows + i] = dbacc[0];
-      else
-        p.db[i] = p.accumulate ? p.db[i] + dbacc[0] : dbacc[0];
+#pragma unroll
+    for (int i = 0; i < DBN; ++i) {
+      const int b = wn + i * T::WN, r = wm * (T::BM / T::WM) + 32 * b + (lane & 31);
+      if (b < T::MB && lane < 32 && r < un.rows) {
+        const int64_t at = out_row0 + r;
+        if (p.splits > 1)
+          p.part_db[un.split * out_rows + at] = dbacc[i][0];
+        else
+          p.db[at] = p.accumulate ? p.db[at] + dbacc[i][0] : dbacc[i][0];
+      }
     }
   }
   if (OP == kWeightGrad && !p.y) return;
-  const float* bias =
-      OP == kForward && p.bias ? p.bias + static_cast<int64_t>(un.g) * p.F : nullptr;
-  constexpr int Q = T::BN / 4;                        // 16-byte chunks per staged row
-  constexpr int WROWS = T::BM / T::WM / T::PASSES;    // staged rows per wave row and pass
+  // In passes through LDS: the fp32 blocks laid down by rows (16-byte chunks
+  // XOR-rotated by the row), then each thread takes eight columns, the same in
+  // every row it takes, of rows RSTEP apart: its bias is loaded once, and
+  // UNROLL rows' residuals and LDS reads are under way together.
+  constexpr int Q = T::BN / 4;                      // 16-byte chunks per staged row
+  constexpr int WROWS = T::BM / T::WM / T::PASSES;  // staged rows per wave row and pass
   constexpr int SROWS = T::BM / T::PASSES;
+  constexpr int CH = T::BN / 8;
+  constexpr int RSTEP = T::THREADS / CH, ITERS = SROWS / RSTEP;
+  constexpr int UNROLL = ITERS % 4 == 0 ? 4 : 2;
+  static_assert(T::THREADS % CH == 0 && SROWS % RSTEP == 0 && ITERS % UNROLL == 0, "copy-out");
   float* const stage = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int pass = 0; pass < T::PASSES; ++pass) {
+  const int c = tid % CH, r0 = tid / CH;
+  const bool live = c * 8 < cols;
+  F8 bias{};
+  if (OP == kForward && p.bias && live && p.splits == 1)
+    bias = load8(p.bias + static_cast<int64_t>(un.g) * p.F + un.col0 + c * 8);
+  auto run_pass = [&](auto PASS) MOE_INLINE {  // a constant: the blocks stay in registers
+    constexpr int pass = decltype(PASS)::value;
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < T::MB / T::PASSES; ++m) {
@@ -448,20 +502,78 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
         }
     }
     __syncthreads();
-    for (int i = tid; i < SROWS * (T::BN / 8); i += T::THREADS) {
-      const int sr = i / (T::BN / 8), c = i % (T::BN / 8);
-      const int row = sr / WROWS * (T::BM / T::WM) + pass * WROWS + sr % WROWS;
-      if (row >= un.rows || c * 8 >= cols) continue;
+    auto take = [&](int sr) MOE_INLINE {
       const f32x4 lo = *reinterpret_cast<const f32x4*>(stage + (sr * Q + ((2 * c) ^ (sr & 15))) * 4);
       const f32x4 hi =
           *reinterpret_cast<const f32x4*>(stage + (sr * Q + ((2 * c + 1) ^ (sr & 15))) * 4);
-      const F8 v{{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}};
-      if (p.splits > 1)
-        store8(p.part + (un.split * out_rows + out_row0 + row) * N + un.col0 + c * 8, v);
+      return F8{{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}};
+    };
+    auto tile_row = [&](int sr) MOE_INLINE {
+      return sr / WROWS * (T::BM / T::WM) + pass * WROWS + sr % WROWS;
+    };
+    auto copy_out = [&](auto each) MOE_INLINE {
+      for (int it = 0; it < ITERS; it += UNROLL) each(r0 + it * RSTEP);
+    };
+    const int64_t at0 = out_row0 * N + un.col0 + c * 8;
+    if (p.splits > 1) {
+      float* part = p.part + un.split * out_rows * N + at0;
+      copy_out([&](int sr0) MOE_INLINE {
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+          const int row = tile_row(sr0 + u * RSTEP);
+          if (row < un.rows && live) store8(part + static_cast<int64_t>(row) * N, take(sr0 + u * RSTEP));
+        }
+      });
+    } else if constexpr (OP == kForward) {
+      auto with_act = [&](auto ACT) MOE_INLINE {
+        copy_out([&](int sr0) MOE_INLINE {
+          F8 res[UNROLL], v[UNROLL];
+#pragma unroll
+          for (int u = 0; u < UNROLL; ++u) {
+            const int row = tile_row(sr0 + u * RSTEP);
+            res[u] = F8{};
+            if (p.residual && row < un.rows && live)
+              res[u] = load8(p.residual + at0 + static_cast<int64_t>(row) * N);
+            v[u] = take(sr0 + u * RSTEP);
+          }
+#pragma unroll
+          for (int u = 0; u < UNROLL; ++u) {
+            const int row = tile_row(sr0 + u * RSTEP);
+            if (row < un.rows && live)
+              finish8<decltype(ACT)::value>(p, v[u], bias, res[u],
+                                            at0 + static_cast<int64_t>(row) * N);
+          }
+        });
+      };
+      // one loop per activation: a switch per element costs more than relu
+      switch (p.act) {
+        case MOE_ACT_RELU: with_act(std::integral_constant<int, MOE_ACT_RELU>{}); break;
+        case MOE_ACT_GELU: with_act(std::integral_constant<int, MOE_ACT_GELU>{}); break;
+        case MOE_ACT_GELU_TANH: with_act(std::integral_constant<int, MOE_ACT_GELU_TANH>{}); break;
+        case MOE_ACT_SILU: with_act(std::integral_constant<int, MOE_ACT_SILU>{}); break;
+        default: with_act(std::integral_constant<int, MOE_ACT_NONE>{}); break;
+      }
+    } else {
+      auto put = [&](auto STREAM) MOE_INLINE {
+        copy_out([&](int sr0) MOE_INLINE {
+#pragma unroll
+          for (int u = 0; u < UNROLL; ++u) {
+            const int row = tile_row(sr0 + u * RSTEP);
+            if (row < un.rows && live)
+              put_grad8<decltype(STREAM)::value>(p, take(sr0 + u * RSTEP),
+                                                 at0 + static_cast<int64_t>(row) * N);
+          }
+        });
+      };
+      if (OP == kWeightGrad && p.stream)
+        put(std::true_type{});
       else
-        finish8(p, v, bias, out_row0 + row, un.col0 + c * 8, N);
+        put(std::false_type{});
     }
-  }
+  };
+  static_assert(T::PASSES <= 2, "passes");
+  run_pass(std::integral_constant<int, 0>{});
+  if constexpr (T::PASSES == 2) run_pass(std::integral_constant<int, 1>{});
 }
 
 }  // namespace

@@ -35,6 +35,7 @@ struct ProductArgs {
   int y_f32;
   int act;                   // MOE_ACT_*
   int accumulate;            // weight gradient: add to y and db
+  int stream;                // weight gradient: y is larger than the last-level cache
   float* db;                 // [G][F] or null (weight gradient)
   // Contraction cut into `splits` ranges whose fp32 sums meet in `part`
   // (kForward, kInputGrad: [splits][P][columns]; kWeightGrad: [splits][G F][K],

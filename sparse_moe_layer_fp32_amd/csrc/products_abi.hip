@@ -3,6 +3,7 @@
 // and the contract are in include/moe.h.
 
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 
 #include "abi_util.h"
@@ -60,16 +61,24 @@ moe_status check_workspace(size_t need, const void* ws, size_t ws_bytes) {
   return MOE_OK;
 }
 
-// Compute units of the current device; an MI355X's 256 where there is none
-// (a workspace can be sized on a host without a GPU).
+// Compute units of the current device, looked up once per device; an
+// MI355X's 256 where there is none (a workspace can be sized on a host
+// without a GPU).
 int device_cus() {
+  static std::atomic<int> known[64];
   int dev = 0, cus = 0;
-  if (hipGetDevice(&dev) != hipSuccess ||
-      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+  if (hipGetDevice(&dev) != hipSuccess) {
+    (void)hipGetLastError();
+    return 256;
+  }
+  const bool slot = dev >= 0 && dev < 64;
+  if (slot && (cus = known[dev].load(std::memory_order_relaxed)) > 0) return cus;
+  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
       cus <= 0) {
     (void)hipGetLastError();
     return 256;
   }
+  if (slot) known[dev].store(cus, std::memory_order_relaxed);
   return cus;
 }
 
