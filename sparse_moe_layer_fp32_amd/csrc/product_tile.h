@@ -184,8 +184,11 @@ struct Tile {
   static constexpr int KS = BK / 16;
   static constexpr int RING = SA * PA::BYTES + SB * PB::BYTES;
   // the fp32 tile leaves in passes that fit the ring
-  static constexpr int PASSES = (BM * BN * 4 + RING - 1) / RING;
-  static_assert(MB >= 1 && NB >= 1 && JA >= 1 && JB >= 1 && MB % PASSES == 0, "tile shape");
+  static constexpr int NEED = (BM * BN * 4 + RING - 1) / RING;
+  static constexpr int PASSES = MB % NEED == 0 ? NEED : MB;
+  static_assert(MB >= 1 && NB >= 1 && JA >= 1 && JB >= 1 && MB % PASSES == 0 &&
+                    BM * BN * 4 / PASSES <= RING,
+                "tile shape");
   static_assert(SA == SB || (SA == 2 && SB > 2), "ring depths");
   static_assert((SB - 1) * (JA + JB) < 64, "vmcnt budget");
 };
@@ -571,9 +574,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
         put(std::false_type{});
     }
   };
-  static_assert(T::PASSES <= 2, "passes");
+  static_assert(T::PASSES <= 3, "passes");
   run_pass(std::integral_constant<int, 0>{});
-  if constexpr (T::PASSES == 2) run_pass(std::integral_constant<int, 1>{});
+  if constexpr (T::PASSES > 1) run_pass(std::integral_constant<int, 1>{});
+  if constexpr (T::PASSES > 2) run_pass(std::integral_constant<int, 2>{});
 }
 
 }  // namespace

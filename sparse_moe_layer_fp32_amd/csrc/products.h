@@ -43,12 +43,16 @@ struct ProductArgs {
   int splits;
   float* part;
   float* part_db;
+  // set by the launcher
+  int cus;
+  int whole, slices;  // Big tiles left whole (-1: all), slices of the rows of the others
 };
 
 // How a product is run: the tile shape and the number of contraction ranges.
 struct ProductPlan {
   int shape;
   int splits;
+  int cus;  // compute units of the device
 };
 ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus);
 // Bytes of `part` (with part_db behind it) for that plan; 0 when splits == 1.

@@ -119,8 +119,26 @@ __device__ __forceinline__ bool find_unit(const ProductArgs& p, int* sh, Unit* u
     __syncthreads();
   }
   if (!p.offsets) un->g = 0;
-  const int u = unit_of_block<OP>(p, total * NT * p.splits);
-  if (u < 0) return false;
+  int part = 0, parts = 1;  // which of how many slices of the tile's rows
+  int u;
+  if (BM == 256 && p.whole >= 0) {
+    // the last tiles, cut into slices of rows, follow the whole ones in
+    // every XCD's order
+    parts = p.slices;
+    const int bid = blockIdx.x, cut = kNumXcd * (p.whole / kNumXcd);
+    if (bid < cut) {
+      u = xcd_remap(bid, cut);
+      parts = 1;
+    } else {
+      const int v = xcd_remap(bid - cut, (total * NT - cut) * parts);
+      if (v < 0) return false;
+      u = cut + v / parts;
+      part = v % parts;
+    }
+  } else {
+    u = unit_of_block<OP>(p, total * NT * p.splits);
+    if (u < 0) return false;
+  }
   un->split = u / (total * NT);
   const int v = u % (total * NT);
   tiles = (n + BM - 1) / BM;
@@ -130,8 +148,9 @@ __device__ __forceinline__ bool find_unit(const ProductArgs& p, int* sh, Unit* u
   const int gm = min(kGroupM, tiles - gfirst);
   const int x = w - gfirst * NT;
   const int rt = gfirst + x % gm;
-  un->row0 = base + rt * BM;
-  un->rows = min(BM, n - rt * BM);
+  un->row0 = base + rt * BM + part * (BM / parts);
+  un->rows = min(BM / parts, n - rt * BM - part * (BM / parts));
+  if (un->rows <= 0) return false;
   un->col0 = x / gm * BN;
   un->begin = base;
   un->len = n;
@@ -146,6 +165,7 @@ __device__ __forceinline__ bool find_unit(const ProductArgs& p, int* sh, Unit* u
 // serves the remainders of groups in Big's launches.
 template <int OP> using Big = Tile<OP, 256, 256, 2, 4, 2, 3>;
 template <int OP> using Half = Tile<OP, 128, 256, 2, 4, 3, 3>;
+template <int OP> using Three = Tile<OP, 192, 256, 2, 4, 2, 3>;
 template <int OP> using Duo = Tile<OP, 256, 128, 2, 2, 3, 3, 32>;
 template <int OP> using Small = Tile<OP, 64, 64, 2, 2, 4, 4>;
 template <int OP> using Flat = Tile<OP, 64, 256, 2, 4, 4, 4>;
@@ -171,6 +191,10 @@ __global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
     }
     if (un.rows <= 128) {
       product_tile<OP, Half<OP>, false, false>(p, smem, un);
+      return;
+    }
+    if (un.rows <= 192) {
+      product_tile<OP, Three<OP>, false, false>(p, smem, un);
       return;
     }
   }
@@ -245,7 +269,9 @@ __global__ __launch_bounds__(64 * kThinWaves) void product_thin(ProductArgs p) {
 // Sums the contraction ranges' partial results in order and finishes them.
 // Thread i: eight consecutive columns of a row; the threads behind the last
 // row: db.
-template <int OP>
+// SPLITS is a constant so that all of a thread's loads are under way at once
+// (a loop over them: 4.7 us for 64 x 4096 from four ranges).
+template <int OP, int SPLITS>
 __global__ __launch_bounds__(256) void product_join(ProductArgs p) {
   const int N = OP == kForward ? p.F : p.K;
   const int64_t rows = OP == kWeightGrad ? static_cast<int64_t>(p.G) * p.F : p.P;
@@ -266,12 +292,14 @@ __global__ __launch_bounds__(256) void product_join(ProductArgs p) {
       if (bias) bias += static_cast<int64_t>(lo) * p.F;
     }
     if (OP == kWeightGrad && !p.y) return;
-    F8 v{};
-    for (int s = 0; s < p.splits; ++s) {
-      const F8 w = load8(p.part + (s * rows + row) * N + col);
+    F8 w[SPLITS];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v.v[q] += w.v[q];
-    }
+    for (int s = 0; s < SPLITS; ++s) w[s] = load8(p.part + (s * rows + row) * N + col);
+    F8 v = w[0];
+#pragma unroll
+    for (int s = 1; s < SPLITS; ++s)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v.v[q] += w[s].v[q];
     if (OP == kForward)
       finish_one(p, v, bias, row, col, N);
     else
@@ -280,7 +308,8 @@ __global__ __launch_bounds__(256) void product_join(ProductArgs p) {
     const int64_t j = i - rows * per_row;
     if (j >= rows) return;
     float v = 0.0f;
-    for (int s = 0; s < p.splits; ++s) v += p.part_db[s * rows + j];
+#pragma unroll
+    for (int s = 0; s < SPLITS; ++s) v += p.part_db[s * rows + j];
     p.db[j] = p.accumulate ? p.db[j] + v : v;
   }
 }
@@ -298,40 +327,67 @@ __global__ __launch_bounds__(256) void source_rows_kernel(const int32_t* __restr
   src[i] = s;
 }
 
-// dz = dy act'(z) and the column sums of each strip of rows: a block takes
-// a strip of 256 x 8 columns, a thread eight columns.
+// dz = dy act'(z) and the column sums of each strip of rows: a block takes a
+// strip of 64 x 8 columns, its four waves every fourth row each, a thread
+// eight columns; the waves' sums meet in LDS.
+//
+// Bound: HBM, 6 bytes an element (4096 x 11264 with GELU and db: 49 us, 5.6
+// TB/s; with a quarter of the blocks, whose threads took 64 rows each, and a
+// column's strips summed by one thread, 110 us).
+constexpr int kStripWaves = 4, kStripCols = 64 * 8;
 int strip_rows(int64_t T) { return 64 * static_cast<int>((T + 65535) / 65536); }
 
-__global__ __launch_bounds__(256) void act_grad_kernel(const uint16_t* __restrict__ dy,
-                                                       const uint16_t* __restrict__ z, int act,
-                                                       int64_t T, int F, uint16_t* __restrict__ dz,
-                                                       float* __restrict__ part, int strip) {
-  const int c = (blockIdx.x * 256 + threadIdx.x) * 8;
-  if (c >= F) return;
+__global__ __launch_bounds__(64 * kStripWaves) void act_grad_kernel(
+    const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, int act, int64_t T, int F,
+    uint16_t* __restrict__ dz, float* __restrict__ part, int strip) {
+  __shared__ __attribute__((aligned(16))) float sums[kStripWaves - 1][kStripCols];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * kStripCols + lane * 8;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * strip;
   const int64_t r1 = min<int64_t>(T, r0 + strip);
   F8 sum{};
+  if (c < F) {
 #pragma unroll 4
-  for (int64_t r = r0; r < r1; ++r) {
-    F8 d = load8(dy + r * F + c);
-    const F8 v = load8(z + r * F + c);
+    for (int64_t r = r0 + wave; r < r1; r += kStripWaves) {
+      F8 d = load8(dy + r * F + c);
+      const F8 v = load8(z + r * F + c);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      d.v[q] *= act_slope(v.v[q], act);
-      sum.v[q] += d.v[q];
+      for (int q = 0; q < 8; ++q) {
+        d.v[q] *= act_slope(v.v[q], act);
+        sum.v[q] += d.v[q];
+      }
+      store8(dz + r * F + c, d);
     }
-    store8(dz + r * F + c, d);
   }
-  if (part) store8(part + static_cast<int64_t>(blockIdx.y) * F + c, sum);
+  if (!part) return;
+  if (wave > 0) store8(&sums[wave - 1][lane * 8], sum);
+  __syncthreads();
+  if (wave > 0 || c >= F) return;
+#pragma unroll
+  for (int w = 0; w < kStripWaves - 1; ++w) {
+    const F8 o = load8(&sums[w][lane * 8]);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum.v[q] += o.v[q];
+  }
+  store8(part + static_cast<int64_t>(blockIdx.y) * F + c, sum);
 }
 
+// The strips' sums, in order: a block takes 64 columns, wave w every fourth strip.
 __global__ __launch_bounds__(256) void strip_sum_kernel(const float* __restrict__ part, int strips,
                                                         int F, float* __restrict__ db,
                                                         int accumulate) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= F) return;
+  __shared__ float sums[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
   float v = 0.0f;
-  for (int s = 0; s < strips; ++s) v += part[static_cast<int64_t>(s) * F + c];
+  if (c < F) {
+#pragma unroll 16
+    for (int s = wave; s < strips; s += 4) v += part[static_cast<int64_t>(s) * F + c];
+  }
+  sums[wave][lane] = v;
+  __syncthreads();
+  if (wave > 0 || c >= F) return;
+  v = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
   db[c] = accumulate ? db[c] + v : v;
 }
 
@@ -354,6 +410,12 @@ int64_t tile_count(int op, int64_t P, int G, int K, int F, bool grouped, ShapeSi
   return (grouped ? P / s.bm + std::min<int64_t>(G, P) : (P + s.bm - 1) / s.bm) * nt;
 }
 
+// Slices of rows that the tiles of a Big launch's last round are cut into.
+int last_round_slices(int64_t units, int cus) {
+  const int64_t last = units % cus;
+  return last == 0 || last * 2 > cus ? 1 : last * 4 > cus ? 2 : 4;
+}
+
 template <int OP>
 unsigned block_count(const ProductArgs& p, int64_t units) {
   return static_cast<unsigned>(OP == kWeightGrad && p.offsets
@@ -367,11 +429,24 @@ hipError_t launch_tiles(const ProductArgs& p, hipStream_t stream) {
       tile_count(OP, p.P, p.G, OP == kWeightGrad && !p.y ? 1 : p.K, p.F, p.offsets != nullptr,
                  {T::BM, T::BN}) * p.splits;
   if (units <= 0) return hipSuccess;
-  const unsigned grid = block_count<OP>(p, units);
+  unsigned grid = block_count<OP>(p, units);
+  ProductArgs q = p;
+  q.whole = -1;
+  if (T::BM == 256 && T::BN == 256 && OP != kWeightGrad && !p.offsets && p.splits == 1) {
+    // Dense Big launches: tiles that would leave half of the GPU idle in the
+    // last round are cut into halves or quarters of their rows.
+    q.slices = last_round_slices(units, p.cus);
+    if (q.slices > 1) {
+      const int64_t last = units % p.cus;
+      q.whole = static_cast<int>(units - last);
+      const int64_t cut = q.whole / kNumXcd * kNumXcd;
+      grid = static_cast<unsigned>(cut + ((units - cut) * q.slices + kNumXcd - 1) / kNumXcd * kNumXcd);
+    }
+  }
   if (OP == kWeightGrad && p.src && p.y)
-    product_kernel<OP, T, OP == kWeightGrad><<<grid, T::THREADS, 0, stream>>>(p);
+    product_kernel<OP, T, OP == kWeightGrad><<<grid, T::THREADS, 0, stream>>>(q);
   else
-    product_kernel<OP, T, false><<<grid, T::THREADS, 0, stream>>>(p);
+    product_kernel<OP, T, false><<<grid, T::THREADS, 0, stream>>>(q);
   return hipGetLastError();
 }
 
@@ -402,7 +477,13 @@ hipError_t launch_op(const ProductArgs& p, int shape, hipStream_t stream) {
   const int N = OP == kForward ? p.F : p.K;
   const int64_t rows = OP == kWeightGrad ? static_cast<int64_t>(p.G) * p.F : p.P;
   const int64_t threads = rows * (N / 8) + (OP == kWeightGrad && p.db ? rows : 0);
-  product_join<OP><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(p);
+  const unsigned grid = static_cast<unsigned>((threads + 255) / 256);
+  switch (p.splits) {
+    case 2: product_join<OP, 2><<<grid, 256, 0, stream>>>(p); break;
+    case 4: product_join<OP, 4><<<grid, 256, 0, stream>>>(p); break;
+    case 8: product_join<OP, 8><<<grid, 256, 0, stream>>>(p); break;
+    default: return hipErrorInvalidValue;
+  }
   return hipGetLastError();
 }
 
@@ -423,6 +504,7 @@ constexpr ShapeCost kCosts[] = {{1, 1.66f, 0.83f, 9.5f},   // Big
                                 {1, 0.98f, 0.49f, 6.2f},   // Half
                                 {2, 2.09f, 0.58f, 5.9f},   // Duo
                                 {2, 0.46f, 0.14f, 2.1f}};  // Small
+constexpr ShapeCost kFlatCost = {1, 0.62f, 0.42f, 5.0f};
 constexpr float kFilling = 0.93f;  // partly grows by this share up to one tile on every CU
 constexpr float kJoin = 2.4f, kJoinBytesPerUs = 7.65e6f;
 
@@ -430,12 +512,19 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
   const int64_t rows = op == kWeightGrad ? static_cast<int64_t>(G) * F : P;
   const int64_t cols = op == kForward ? F : K;
   const int64_t L = op == kForward ? K : op == kInputGrad ? F : (P + G - 1) / G;
-  // Tiles as they will be, about: a group with rows has half a tile more.
+  // Few rows a group: every shape streams the weights at HBM rate, Small a
+  // little faster (64 tokens on 8 of 288 experts, 4096 -> 1280: 235 us; Big
+  // 246, Half 243).
+  if (op != kWeightGrad && G > 1 && P > kThinRows && P <= 16 * static_cast<int64_t>(G))
+    return {kShapeSmall, 1, cus};
+  // Tiles as they will be, about: a group with rows has half a tile more (Big,
+  // whose launches give remainders smaller tiles: a quarter).
   const bool ragged = G > 1;
   auto tiles_of = [&](int s) {
     int64_t n = tile_count(op, P, G, K, F, false, kShapeSizes[s]);
     if (op != kWeightGrad && ragged)
-      n += (std::min<int64_t>(G, P) + 1) / 2 * ((cols + kShapeSizes[s].bn - 1) / kShapeSizes[s].bn);
+      n += (std::min<int64_t>(G, P) + 1) / (s == kShapeBig ? 4 : 2) *
+           ((cols + kShapeSizes[s].bn - 1) / kShapeSizes[s].bn);
     return n;
   };
   const int64_t steps = std::max<int64_t>(1, (L + 63) / 64);
@@ -443,8 +532,8 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
   // weigh little (16 x 4096 -> 4096: 11.4 us against 13.8 for the best tile
   // and split; 16 x 11264 -> 4096: 27.6 against 23.8).
   if (op == kForward && P <= kThinRows && P * K <= 98304)
-    return {tiles_of(kShapeThin16) <= cus / 2 ? kShapeThin8 : kShapeThin16, 1};
-  ProductPlan best{kShapeSmall, 1};
+    return {tiles_of(kShapeThin16) <= cus / 2 ? kShapeThin8 : kShapeThin16, 1, cus};
+  ProductPlan best{kShapeSmall, 1, cus};
   float best_us = 0.0f;
   for (int s = kShapeBig; s <= kShapeSmall; ++s) {
     const ShapeCost& c = kCosts[s];
@@ -457,13 +546,18 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
         us = static_cast<float>(units) / slots * (n * c.full + c.fixed);
       else if (rest > cus)
         us += n * c.full + c.fixed;
-      else if (rest)
-        us += n * c.partly * (1.0f + kFilling * static_cast<float>(rest) / cus) + c.fixed;
+      else if (rest) {
+        const int slices = s == kShapeBig && op != kWeightGrad && !ragged && splits == 1
+                               ? last_round_slices(units, cus)
+                               : 1;
+        const ShapeCost& l = slices == 4 ? kFlatCost : slices == 2 ? kCosts[kShapeHalf] : c;
+        us += n * l.partly * (1.0f + kFilling * static_cast<float>(rest * slices) / cus) + l.fixed;
+      }
       if (splits > 1)
         us += kJoin + static_cast<float>(rows) * cols * (8.0f * splits + 4.0f) / kJoinBytesPerUs;
       if (best_us == 0.0f || us < best_us) {
         best_us = us;
-        best = {s, splits};
+        best = {s, splits, cus};
       }
     }
   }
@@ -481,6 +575,7 @@ hipError_t launch_product(int op, const ProductArgs& p, const ProductPlan& plan,
                           hipStream_t stream) {
   ProductArgs q = p;
   q.splits = plan.splits;
+  q.cus = plan.cus;
   if (op == kForward) return launch_op<kForward>(q, plan.shape, stream);
   if (op == kInputGrad) return launch_op<kInputGrad>(q, plan.shape, stream);
   // A weight gradient that will not stay in the 256 MB last-level cache is
@@ -507,12 +602,12 @@ hipError_t launch_act_grad(const uint16_t* dy, const uint16_t* z, int act, int64
                            uint16_t* dz, float* db, int accumulate, float* part,
                            hipStream_t stream) {
   const int rows = strip_rows(T), strips = static_cast<int>((T + rows - 1) / rows);
-  const dim3 grid((F / 8 + 255) / 256, strips);
-  act_grad_kernel<<<grid, 256, 0, stream>>>(dy, z, act, T, F, dz, db ? part : nullptr,
-                                       rows);
+  const dim3 grid((F + kStripCols - 1) / kStripCols, strips);
+  act_grad_kernel<<<grid, 64 * kStripWaves, 0, stream>>>(dy, z, act, T, F, dz,
+                                                         db ? part : nullptr, rows);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !db) return e;
-  strip_sum_kernel<<<(F + 255) / 256, 256, 0, stream>>>(part, strips, F, db, accumulate);
+  strip_sum_kernel<<<(F + 63) / 64, 256, 0, stream>>>(part, strips, F, db, accumulate);
   return hipGetLastError();
 }
 

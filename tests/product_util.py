@@ -76,6 +76,11 @@ def f32(*shape, scale=1.0, seed=0):
     return torch.randn(*shape, generator=g) * scale
 
 
+def d64(t):
+    """On the GPU in 64 bits, where the references are formed."""
+    return t.cuda().double()
+
+
 class Guarded:
     """A device tensor inside a larger buffer whose surroundings are a
     sentinel (outputs: writes outside show) or NaN (inputs: reads outside
@@ -109,7 +114,7 @@ def inp(host):
 
 def within(got, want, bound, what):
     """got (any dtype) against want in 64 bits, element by element."""
-    err = (got.double() - want).abs()
+    err = (got.to(want.device).double() - want).abs()
     bad = ~(err <= bound)
     if bad.any():
         i = int(torch.where(bad, err - bound, torch.full_like(err, -1)).flatten().argmax())

@@ -8,7 +8,7 @@ import torch
 
 from tests import gpu_util as gu
 from tests import product_util as pu
-from tests.product_util import Guarded, bf16, f32, half, inp, sum_err, within
+from tests.product_util import Guarded, bf16, d64, f32, half, inp, sum_err, within
 
 pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -47,18 +47,18 @@ def check_linear_forward(moe, T, K, F, act="none", y_dtype="bf16", bias=True, re
     z = Guarded(shape=(T, F), dtype=torch.bfloat16) if keep_z else None
     moe.moe_linear_forward(cfg, inp(x), inp(w), inp(b), inp(r), y.t, z.t if z else None, ws)
     torch.cuda.synchronize()
-    xd, wd = x.double(), w.double()
+    xd, wd = d64(x), d64(w)
     zd = xd @ wd.t()
     mag = xd.abs() @ wd.abs().t()
     if bias:
-        zd, mag = zd + b.double(), mag + b.double().abs()
+        zd, mag = zd + d64(b), mag + d64(b).abs()
     zerr = sum_err(K, mag)
     if keep_z:
         within(z.check(), zd, (1 + pu.BF16_HALF) * zerr + pu.BF16_HALF * zd.abs(), "z")
     yd = pu.act(zd, act)
     err = pu.MAX_SLOPE[act] * zerr + pu.act_err(zd, act)
     if residual:
-        yd = yd + r.double()
+        yd = yd + d64(r)
         err = err + 2.0 ** -23 * yd.abs()
     h = half(DT[y_dtype])
     within(y.check(), yd, (1 + h) * err + h * yd.abs(), "y")
@@ -67,6 +67,16 @@ def check_linear_forward(moe, T, K, F, act="none", y_dtype="bf16", bias=True, re
 @pytest.mark.parametrize("T,K,F", LINEAR)
 def test_linear_forward_sizes(moe, T, K, F):
     check_linear_forward(moe, T, K, F)
+
+
+# Sizes at which an MI355X's launches take each tile shape (256 x 256, 128 x
+# 256, 256 x 128, 64 x 64), contraction split (up to 8 ranges) and cut of the
+# last round's tiles (halves, quarters).
+@pytest.mark.parametrize("T,K,F", [
+    (1500, 72, 4096), (5000, 520, 4200), (4100, 520, 4104), (4100, 136, 1032), (1000, 4096, 2056),
+    (4100, 72, 1032), (9000, 4096, 72), (2100, 4096, 72), (1500, 2056, 72), (300, 2056, 72)])
+def test_linear_forward_shapes(moe, T, K, F):
+    check_linear_forward(moe, T, K, F, "silu", keep_z=False, seed=7)
 
 
 @pytest.mark.parametrize("act,y_dtype", itertools.product(
@@ -99,33 +109,48 @@ def check_linear_backward(moe, T, K, F, act="none", dw_dtype="f32", accumulate=F
                             inp(x) if dw else None, inp(w) if dx else None, t(dz), t(dx), t(dw),
                             t(db), ws)
     torch.cuda.synchronize()
-    zd = z.double()
+    zd = d64(z)
     sl = pu.slope(zd, act)
-    dzd, dzerr = dy.double() * sl, dy.double().abs() * pu.slope_err(zd, act) + 2.0 ** -24 * (
-        dy.double() * sl).abs()
-    used = dy.double()  # what dx and dw are formed from
+    dyd = d64(dy)
+    dzd, dzerr = dyd * sl, dyd.abs() * pu.slope_err(zd, act) + 2.0 ** -24 * (dyd * sl).abs()
+    used = dyd  # what dx and dw are formed from
     if dz:
         got = dz.check()
         within(got, dzd, (1 + pu.BF16_HALF) * dzerr + pu.BF16_HALF * dzd.abs(), "dz")
-        used = got.double()
+        used = d64(got)
     if dx:
-        want_, mag = used @ w.double(), used.abs() @ w.double().abs()
+        want_, mag = used @ d64(w), used.abs() @ d64(w).abs()
         within(dx.check(), want_, 1.01 * sum_err(F, mag) + pu.BF16_HALF * want_.abs(), "dx")
     if dw:
-        want_, mag = used.t() @ x.double(), used.abs().t() @ x.double().abs()
+        want_, mag = used.t() @ d64(x), used.abs().t() @ d64(x).abs()
         if accumulate:
-            want_, mag = want_ + dw0.double(), mag + dw0.double().abs()
+            want_, mag = want_ + d64(dw0), mag + d64(dw0).abs()
         within(dw.check(), want_, 1.01 * sum_err(T, mag) + half(DT[dw_dtype]) * want_.abs(), "dw")
     if db:
         want_, mag = dzd.sum(0), dzd.abs().sum(0)
         if accumulate:
-            want_, mag = want_ + db0.double(), mag + db0.double().abs()
+            want_, mag = want_ + d64(db0), mag + d64(db0).abs()
         within(db.check(), want_, sum_err(T, mag) + dzerr.sum(0), "db")
 
 
 @pytest.mark.parametrize("T,K,F", LINEAR)
 def test_linear_backward_sizes(moe, T, K, F):
     check_linear_backward(moe, T, K, F)
+
+
+@pytest.mark.parametrize("T,K,F", [  # as above, for the input gradient
+    (1500, 4096, 72), (5000, 4200, 520), (4100, 4104, 520), (4100, 1032, 136), (1000, 2056, 4096),
+    (4100, 1032, 72), (2100, 72, 4096), (1500, 72, 2056), (300, 72, 2056)])
+def test_linear_input_gradient_shapes(moe, T, K, F):
+    check_linear_backward(moe, T, K, F, want=("dx",), seed=7)
+
+
+@pytest.mark.parametrize("T,K,F", [  # and for the weight gradient
+    (300, 2056, 4096), (9000, 520, 4096), (300, 4096, 4096), (4100, 264, 4096), (9000, 264, 2056),
+    (300, 1032, 4096), (3000, 1032, 2056), (3000, 1032, 1032), (9000, 520, 1032),
+    (3000, 72, 2056), (2100, 72, 1032), (1500, 72, 72)])
+def test_linear_weight_gradient_shapes(moe, T, K, F):
+    check_linear_backward(moe, T, K, F, want=("dw", "db"), seed=7)
 
 
 @pytest.mark.parametrize("act", ("relu", "gelu", "gelu_tanh", "silu"))
@@ -203,6 +228,16 @@ def spans(off):
     return [(e, int(off[e]), int(off[e + 1])) for e in range(len(off) - 1)]
 
 
+def source_rows(x, ids, P):
+    """The rows that rows 0 .. P - 1 read, in 64 bits: zeros for a source
+    outside x."""
+    if ids is None:
+        return d64(x)
+    s = torch.where(ids >= 0, torch.div(ids, 3, rounding_mode="floor"), -1).long().cuda()
+    ok = (s >= 0) & (s < x.shape[0])
+    return d64(x)[s.clamp(0, x.shape[0] - 1)] * ok.unsqueeze(1)
+
+
 def check_grouped_forward(moe, sizes, K, F, before=0, after=0, gather=True, bias=True,
                           y_dtype="bf16", bad_ids=(), seed=0):
     P, T, off, ids = group_case(sizes, before, after, K, seed=seed)
@@ -222,20 +257,16 @@ def check_grouped_forward(moe, sizes, K, F, before=0, after=0, gather=True, bias
     torch.cuda.synchronize()
     got = y.check()
     h = half(DT[y_dtype])
-    rows = torch.zeros(P, K, dtype=torch.double)
-    for r in range(P):
-        s = r if ids is None else int(ids[r]) // 3 if int(ids[r]) >= 0 else -1
-        if 0 <= s < T:
-            rows[r] = x[s].double()
+    rows = source_rows(x, ids, P)
     seen = torch.zeros(P, dtype=torch.bool)
     for e, i, j in spans(off):
         seen[i:j] = True
         if j == i:
             continue
-        want = rows[i:j] @ w[e].double().t()
-        mag = rows[i:j].abs() @ w[e].double().abs().t()
+        want = rows[i:j] @ d64(w[e]).t()
+        mag = rows[i:j].abs() @ d64(w[e]).abs().t()
         if bias:
-            want, mag = want + b[e].double(), mag + b[e].double().abs()
+            want, mag = want + d64(b[e]), mag + d64(b[e]).abs()
         within(got[i:j], want, (1 + h) * sum_err(K, mag) + h * want.abs(), f"y of group {e}")
     assert (got[~seen] == pu.SENTINEL).all(), "a row of no group was written"
 
@@ -244,6 +275,40 @@ def check_grouped_forward(moe, sizes, K, F, before=0, after=0, gather=True, bias
 @pytest.mark.parametrize("K,F", [(72, 136), (512, 264)])
 def test_grouped_forward(moe, name, K, F):
     check_grouped_forward(moe, GROUPS[name], K, F)
+
+
+UNEVEN = [1500, 0, 700, 60, 2400, 130, 190, 250, 1, 400, 2000, 369]  # 8000 rows
+
+
+@pytest.mark.parametrize("sizes,K,F", [
+    (UNEVEN, 1032, 2056), ([3000, 900, 2100], 72, 1032), ([1500, 1, 640, 900, 1400, 1300, 259], 72, 1032),
+    ([2, 0, 1, 5, 3], 2056, 520)])
+def test_grouped_forward_shapes(moe, sizes, K, F):
+    """256 x 256 tiles with every size of remainder, the other shapes, and
+    few rows."""
+    check_grouped_forward(moe, sizes, K, F, before=3, after=70, seed=7)
+
+
+@pytest.mark.parametrize("sizes,K,F", [
+    (UNEVEN, 2056, 1032), ([6000, 1, 5999], 520, 136), ([2500, 900, 2600], 1032, 136)])
+def test_grouped_input_gradient_shapes(moe, sizes, K, F):
+    check_grouped_backward(moe, sizes, K, F, before=3, after=70, want=("dx",), seed=7)
+
+
+@pytest.mark.parametrize("sizes,K,F", [
+    ([(i * 29) % 61 for i in range(40)], 520, 520), ([100, 0, 300, 1, 640, 209], 1032, 1032),
+    ([9000, 3, 2997], 1032, 1032), ([700, 2300, 3000], 72, 136), ([5000, 6000, 1000], 72, 1032)])
+@pytest.mark.parametrize("gather", (False, True))
+def test_grouped_weight_gradient_shapes(moe, sizes, K, F, gather):
+    check_grouped_backward(moe, sizes, K, F, before=3, after=70, gather=gather, want=("dw", "db"),
+                           seed=7)
+
+
+@pytest.mark.parametrize("accumulate", (False, True))
+def test_grouped_weight_gradient_larger_than_the_caches(moe, accumulate):
+    """Above 256 MB the gradient is stored past the caches."""
+    check_grouped_backward(moe, [(i * 29) % 61 for i in range(64)], 1032, 1032,
+                           accumulate=accumulate, want=("dw", "db"), seed=8)
 
 
 @pytest.mark.parametrize("gather,bias,y_dtype", itertools.product((False, True), (False, True),
@@ -301,29 +366,25 @@ def check_grouped_backward(moe, sizes, K, F, before=0, after=0, gather=True, dw_
     moe.moe_grouped_backward(cfg, inp(dy), inp(x), inp(ids), inp(off), inp(w), t(dx), t(dw), t(db),
                              ws)
     torch.cuda.synchronize()
-    rows = torch.zeros(P, K, dtype=torch.double)
-    for r in range(P):
-        s = r if ids is None else int(ids[r]) // 3 if int(ids[r]) >= 0 else -1
-        if 0 <= s < T:
-            rows[r] = x[s].double()
+    rows = source_rows(x, ids, P)
     gx, gw, gb = (g.check() if g else None for g in (dx, dw, db))
     seen = torch.zeros(P, dtype=torch.bool)
     for e, i, j in spans(off):
         seen[i:j] = True
-        d, xe = dy[i:j].double(), rows[i:j]
+        d, xe = d64(dy[i:j]), rows[i:j]
         if dx and j > i:
-            want_, mag = d @ w[e].double(), d.abs() @ w[e].double().abs()
+            want_, mag = d @ d64(w[e]), d.abs() @ d64(w[e]).abs()
             within(gx[i:j], want_, 1.01 * sum_err(F, mag) + pu.BF16_HALF * want_.abs(), f"dx {e}")
         if dw:
             want_, mag = d.t() @ xe, d.abs().t() @ xe.abs()
             if accumulate:
-                want_, mag = want_ + dw0[e].double(), mag + dw0[e].double().abs()
+                want_, mag = want_ + d64(dw0[e]), mag + d64(dw0[e]).abs()
             within(gw[e], want_, 1.01 * sum_err(j - i, mag) + half(DT[dw_dtype]) * want_.abs(),
                    f"dw {e}")
         if db:
             want_, mag = d.sum(0), d.abs().sum(0)
             if accumulate:
-                want_, mag = want_ + db0[e].double(), mag + db0[e].double().abs()
+                want_, mag = want_ + d64(db0[e]), mag + d64(db0[e]).abs()
             within(gb[e], want_, sum_err(j - i, mag), f"db {e}")
     if dx:
         assert (gx[~seen] == pu.SENTINEL).all(), "a row of no group was written"
