@@ -1,205 +1,16 @@
 // Linear and grouped products on gfx950 matrix cores: y = x W^T with bias,
 // activation and residual, and the gradients dx = dy W and dW = dy^T x, for
 // one group of rows or for one group per expert with ragged sizes.  The tile
-// itself (mainloop and epilogue) is in product_tile.h; this file finds each
-// block's tile, chooses tile shapes and joins split contractions.
+// itself (mainloop and epilogue) is in product_tile.h, each block's share of
+// the work in product_blocks.h, the gradients' launches in product_grads.hip
+// and product_pairs.hip; this file holds the forward product, the choice of
+// tile shapes and the elementwise kernels.
 
-#include <algorithm>
-
-#include "product_tile.h"
+#include "product_blocks.h"
 
 namespace moe {
 
 namespace {
-
-constexpr int kGroupM = 8;  // row tiles walked together, so that they share column operands
-
-__device__ __forceinline__ int clamp_row(int v, int64_t P) {
-  return static_cast<int>(min<int64_t>(max(v, 0), P));
-}
-
-// Block -> unit.  One group: each XCD takes a contiguous range (xcd_remap).
-// Ragged groups: runs of kRun units dealt over the XCDs in turn, since
-// contiguous ranges of experts of different sizes leave some XCDs long behind
-// the others.  Returns -1 for a block without work.
-constexpr int kRun = 16;
-__host__ __device__ __forceinline__ int64_t run_grid(int64_t units) {
-  return (units + kRun * kNumXcd - 1) / (kRun * kNumXcd) * (kRun * kNumXcd);
-}
-template <int OP>
-__device__ __forceinline__ int unit_of_block(const ProductArgs& p, int nvalid) {
-  const int bid = blockIdx.x;
-  if (OP != kWeightGrad || !p.offsets) return xcd_remap(bid, nvalid);
-  const int xcd = bid % kNumXcd, slot = bid / kNumXcd;
-  const int u = (slot / kRun * kNumXcd + xcd) * kRun + slot % kRun;
-  return u < nvalid ? u : -1;
-}
-
-// The block's unit, false if it has none.  Forward and input gradient: the
-// tiles of a group number ceil(rows / BM), known on the device only, so the
-// block prefixes the groups' tile counts itself (at most 1024 groups, a few
-// per thread) -- about 1 us, against a launch and a tile list in memory.
-template <int OP, int BM, int BN, int THREADS>
-__device__ __forceinline__ bool find_unit(const ProductArgs& p, int* sh, Unit* un) {
-  const int tid = threadIdx.x;
-  const int N = OP == kForward ? p.F : p.K;
-  // db alone (no y): one column tile
-  const int NT = OP == kWeightGrad && !p.y ? 1 : (N + BN - 1) / BN;
-  if constexpr (OP == kWeightGrad) {
-    const int MT = (p.F + BM - 1) / BM;
-    const int per = p.G * MT * NT;
-    const int u = unit_of_block<OP>(p, per * p.splits);
-    if (u < 0) return false;
-    un->split = u / per;
-    const int v = u % per;
-    un->g = v / (MT * NT);
-    const int t = v % (MT * NT);
-    const int first = t / (kGroupM * NT) * kGroupM;
-    const int gm = min(kGroupM, MT - first);
-    const int w = t - first * NT;
-    un->row0 = (first + w % gm) * BM;
-    un->rows = min(BM, p.F - un->row0);
-    un->col0 = w / gm * BN;
-    un->begin = p.offsets ? clamp_row(p.offsets[un->g], p.P) : 0;
-    const int end = p.offsets ? clamp_row(p.offsets[un->g + 1], p.P) : static_cast<int>(p.P);
-    un->len = max(0, end - un->begin);
-    return true;
-  }
-  int tiles, base = 0, n = static_cast<int>(p.P), first_tile = 0, total;
-  if (!p.offsets) {
-    total = static_cast<int>((p.P + BM - 1) / BM);
-  } else {
-    const int c = (p.G + THREADS - 1) / THREADS;
-    int mine = 0;
-    for (int i = tid * c; i < min(tid * c + c, p.G); ++i) {
-      const int b = clamp_row(p.offsets[i], p.P);
-      mine += (max(0, clamp_row(p.offsets[i + 1], p.P) - b) + BM - 1) / BM;
-    }
-    const int lane = tid & 63, wid = tid >> 6;
-    int incl = mine;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(incl, off);
-      if (lane >= off) incl += o;
-    }
-    if (lane == 63) sh[wid] = incl;
-    __syncthreads();
-    int before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 64; ++w) {
-      if (w < wid) before += sh[w];
-      total += sh[w];
-    }
-    total = __builtin_amdgcn_readfirstlane(total);
-    const int u = unit_of_block<OP>(p, total * NT * p.splits);
-    if (u < 0) return false;
-    int t = u % (total * NT) / NT;
-    int at = before + incl - mine;
-    if (t >= at && t < at + mine) {
-      for (int i = tid * c; i < min(tid * c + c, p.G); ++i) {
-        const int b = clamp_row(p.offsets[i], p.P);
-        const int rows = max(0, clamp_row(p.offsets[i + 1], p.P) - b);
-        const int k = (rows + BM - 1) / BM;
-        if (t < at + k) {
-          sh[16] = i;
-          sh[17] = b;
-          sh[18] = rows;
-          sh[19] = at;
-          break;
-        }
-        at += k;
-      }
-    }
-    __syncthreads();
-    un->g = __builtin_amdgcn_readfirstlane(sh[16]);
-    base = __builtin_amdgcn_readfirstlane(sh[17]);
-    n = __builtin_amdgcn_readfirstlane(sh[18]);
-    first_tile = __builtin_amdgcn_readfirstlane(sh[19]);
-    __syncthreads();
-  }
-  if (!p.offsets) un->g = 0;
-  int part = 0, parts = 1;  // which of how many slices of the tile's rows
-  int u;
-  if (BM == 256 && p.whole >= 0) {
-    // the last tiles, cut into slices of rows, follow the whole ones in
-    // every XCD's order
-    parts = p.slices;
-    const int bid = blockIdx.x, cut = kNumXcd * (p.whole / kNumXcd);
-    if (bid < cut) {
-      u = xcd_remap(bid, cut);
-      parts = 1;
-    } else {
-      const int v = xcd_remap(bid - cut, (total * NT - cut) * parts);
-      if (v < 0) return false;
-      u = cut + v / parts;
-      part = v % parts;
-    }
-  } else {
-    u = unit_of_block<OP>(p, total * NT * p.splits);
-    if (u < 0) return false;
-  }
-  un->split = u / (total * NT);
-  const int v = u % (total * NT);
-  tiles = (n + BM - 1) / BM;
-  // inside the group: runs of kGroupM row tiles, the row tile fastest
-  const int w = v - first_tile * NT;
-  const int gfirst = w / (kGroupM * NT) * kGroupM;
-  const int gm = min(kGroupM, tiles - gfirst);
-  const int x = w - gfirst * NT;
-  const int rt = gfirst + x % gm;
-  un->row0 = base + rt * BM + part * (BM / parts);
-  un->rows = min(BM / parts, n - rt * BM - part * (BM / parts));
-  if (un->rows <= 0) return false;
-  un->col0 = x / gm * BN;
-  un->begin = base;
-  un->len = n;
-  return true;
-}
-
-// Tile shapes of the ring-buffered mainloop.  Big: many rows, whole rounds of
-// the GPU; 8 waves of 128 x 64, A 2 and B 3 stages deep (160 KB of LDS).
-// Duo: two blocks of four such waves a CU, so that one's start and epilogue
-// overlap the other's products, at 1.5 times the operand traffic: short
-// contractions.  Half and Small: fewer rows or columns, more blocks.  Flat
-// serves the remainders of groups in Big's launches.
-template <int OP> using Big = Tile<OP, 256, 256, 2, 4, 2, 3>;
-template <int OP> using Half = Tile<OP, 128, 256, 2, 4, 3, 3>;
-template <int OP> using Three = Tile<OP, 192, 256, 2, 4, 2, 3>;
-template <int OP> using Duo = Tile<OP, 256, 128, 2, 2, 3, 3, 32>;
-template <int OP> using Small = Tile<OP, 64, 64, 2, 2, 4, 4>;
-template <int OP> using Flat = Tile<OP, 64, 256, 2, 4, 4, 4>;
-
-template <int OP, class T, bool GATHER>
-__global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::RING];
-  Unit un;
-  if (!find_unit<OP, T::BM, T::BN, T::THREADS>(p, reinterpret_cast<int*>(smem), &un)) return;
-  if constexpr (OP == kWeightGrad) {
-    if (p.accumulate && un.len == 0 && p.splits == 1) return;
-    if (p.db && un.col0 == 0) {
-      product_tile<OP, T, GATHER, true>(p, smem, un);
-      return;
-    }
-  } else if constexpr (T::BM == 256 && T::BN == 256) {
-    // the remainder of a group: the same columns with fewer rows
-    static_assert(Half<OP>::RING <= T::RING && Flat<OP>::RING <= T::RING, "the same LDS");
-    static_assert(Half<OP>::THREADS == T::THREADS && Flat<OP>::THREADS == T::THREADS, "and waves");
-    if (un.rows <= 64) {
-      product_tile<OP, Flat<OP>, false, false>(p, smem, un);
-      return;
-    }
-    if (un.rows <= 128) {
-      product_tile<OP, Half<OP>, false, false>(p, smem, un);
-      return;
-    }
-    if (un.rows <= 192) {
-      product_tile<OP, Three<OP>, false, false>(p, smem, un);
-      return;
-    }
-  }
-  product_tile<OP, T, GATHER, false>(p, smem, un);
-}
 
 // Few rows (a token, or some): the product streams W once and is bound by
 // that stream and by latency, so nothing goes through LDS on the way.  A block
@@ -213,14 +24,15 @@ __global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
 // takes 6.3 us instead of 7.6, while 1 x 4096 -> 4096, whose 256 pieces of 16
 // fill the GPU, takes 9.6 instead of 8.0.  64-byte pieces of W, or the
 // non-temporal hint, cost 8% more (lines fetched twice).
-constexpr int kThinRows = 16, kThinWaves = 8;
+constexpr int kThinWaves = 8;
 constexpr int kThinAhead = 4;  // lines of each row that a wave requests before it multiplies
 
 template <int COLS>
 __global__ __launch_bounds__(64 * kThinWaves) void product_thin(ProductArgs p) {
   __shared__ __attribute__((aligned(16))) float sums[kThinWaves * 256];
   Unit un;
-  if (!find_unit<kForward, kThinRows, COLS, 64 * kThinWaves>(p, reinterpret_cast<int*>(sums), &un))
+  if (!find_unit<kForward, kThinRows, COLS, 64 * kThinWaves>(p, blockIdx.x, reinterpret_cast<int*>(sums),
+                                                       &un))
     return;
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
@@ -264,54 +76,6 @@ __global__ __launch_bounds__(64 * kThinWaves) void product_thin(ProductArgs p) {
   }
   finish_one(p, v, p.bias ? p.bias + static_cast<int64_t>(un.g) * p.F : nullptr, un.row0 + row,
              un.col0 + c, p.F);
-}
-
-// Sums the contraction ranges' partial results in order and finishes them.
-// Thread i: eight consecutive columns of a row; the threads behind the last
-// row: db.
-// SPLITS is a constant so that all of a thread's loads are under way at once
-// (a loop over them: 4.7 us for 64 x 4096 from four ranges).
-template <int OP, int SPLITS>
-__global__ __launch_bounds__(256) void product_join(ProductArgs p) {
-  const int N = OP == kForward ? p.F : p.K;
-  const int64_t rows = OP == kWeightGrad ? static_cast<int64_t>(p.G) * p.F : p.P;
-  const int per_row = N / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t row = i / per_row;
-  if (row < rows) {
-    const int col = static_cast<int>(i - row * per_row) * 8;
-    const float* bias = p.bias;
-    if (OP != kWeightGrad && p.offsets) {
-      // the group whose rows hold this one: the last with offset <= row
-      if (row < clamp_row(p.offsets[0], p.P) || row >= clamp_row(p.offsets[p.G], p.P)) return;
-      int lo = 0, hi = p.G;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.offsets[mid] <= row) lo = mid; else hi = mid;
-      }
-      if (bias) bias += static_cast<int64_t>(lo) * p.F;
-    }
-    if (OP == kWeightGrad && !p.y) return;
-    F8 w[SPLITS];
-#pragma unroll
-    for (int s = 0; s < SPLITS; ++s) w[s] = load8(p.part + (s * rows + row) * N + col);
-    F8 v = w[0];
-#pragma unroll
-    for (int s = 1; s < SPLITS; ++s)
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v.v[q] += w[s].v[q];
-    if (OP == kForward)
-      finish_one(p, v, bias, row, col, N);
-    else
-      put_grad8<false>(p, v, row * N + col);
-  } else if (OP == kWeightGrad && p.db) {
-    const int64_t j = i - rows * per_row;
-    if (j >= rows) return;
-    float v = 0.0f;
-#pragma unroll
-    for (int s = 0; s < SPLITS; ++s) v += p.part_db[s * rows + j];
-    p.db[j] = p.accumulate ? p.db[j] + v : v;
-  }
 }
 
 __global__ __launch_bounds__(256) void source_rows_kernel(const int32_t* __restrict__ row_ids,
@@ -391,65 +155,6 @@ __global__ __launch_bounds__(256) void strip_sum_kernel(const float* __restrict_
   db[c] = accumulate ? db[c] + v : v;
 }
 
-enum Shape : int {
-  kShapeBig, kShapeHalf, kShapeDuo, kShapeSmall,
-  kShapeThin8, kShapeThin16,  // forward only: product_thin
-  kNumShapes
-};
-
-struct ShapeSize {
-  int bm, bn;
-};
-constexpr ShapeSize kShapeSizes[kNumShapes] = {{256, 256}, {128, 256},     {256, 128},
-                                               {64, 64},   {kThinRows, 8}, {kThinRows, 16}};
-
-// Tiles of a product, at most (the tiles of ragged groups are counted on the device).
-int64_t tile_count(int op, int64_t P, int G, int K, int F, bool grouped, ShapeSize s) {
-  const int64_t nt = ((op == kForward ? F : K) + s.bn - 1) / s.bn;
-  if (op == kWeightGrad) return static_cast<int64_t>(G) * ((F + s.bm - 1) / s.bm) * nt;
-  return (grouped ? P / s.bm + std::min<int64_t>(G, P) : (P + s.bm - 1) / s.bm) * nt;
-}
-
-// Slices of rows that the tiles of a Big launch's last round are cut into.
-int last_round_slices(int64_t units, int cus) {
-  const int64_t last = units % cus;
-  return last == 0 || last * 2 > cus ? 1 : last * 4 > cus ? 2 : 4;
-}
-
-template <int OP>
-unsigned block_count(const ProductArgs& p, int64_t units) {
-  return static_cast<unsigned>(OP == kWeightGrad && p.offsets
-                                   ? run_grid(units)
-                                   : (units + kNumXcd - 1) / kNumXcd * kNumXcd);
-}
-
-template <int OP, class T>
-hipError_t launch_tiles(const ProductArgs& p, hipStream_t stream) {
-  const int64_t units =
-      tile_count(OP, p.P, p.G, OP == kWeightGrad && !p.y ? 1 : p.K, p.F, p.offsets != nullptr,
-                 {T::BM, T::BN}) * p.splits;
-  if (units <= 0) return hipSuccess;
-  unsigned grid = block_count<OP>(p, units);
-  ProductArgs q = p;
-  q.whole = -1;
-  if (T::BM == 256 && T::BN == 256 && OP != kWeightGrad && !p.offsets && p.splits == 1) {
-    // Dense Big launches: tiles that would leave half of the GPU idle in the
-    // last round are cut into halves or quarters of their rows.
-    q.slices = last_round_slices(units, p.cus);
-    if (q.slices > 1) {
-      const int64_t last = units % p.cus;
-      q.whole = static_cast<int>(units - last);
-      const int64_t cut = q.whole / kNumXcd * kNumXcd;
-      grid = static_cast<unsigned>(cut + ((units - cut) * q.slices + kNumXcd - 1) / kNumXcd * kNumXcd);
-    }
-  }
-  if (OP == kWeightGrad && p.src && p.y)
-    product_kernel<OP, T, OP == kWeightGrad><<<grid, T::THREADS, 0, stream>>>(q);
-  else
-    product_kernel<OP, T, false><<<grid, T::THREADS, 0, stream>>>(q);
-  return hipGetLastError();
-}
-
 template <int COLS>
 hipError_t launch_thin(const ProductArgs& p, hipStream_t stream) {
   const int64_t units =
@@ -460,34 +165,13 @@ hipError_t launch_thin(const ProductArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int OP>
-hipError_t launch_op(const ProductArgs& p, int shape, hipStream_t stream) {
-  hipError_t e;
-  if constexpr (OP == kForward) {
-    if (shape == kShapeThin8) return launch_thin<8>(p, stream);
-    if (shape == kShapeThin16) return launch_thin<16>(p, stream);
-  }
-  switch (shape) {
-    case kShapeBig: e = launch_tiles<OP, Big<OP>>(p, stream); break;
-    case kShapeHalf: e = launch_tiles<OP, Half<OP>>(p, stream); break;
-    case kShapeDuo: e = launch_tiles<OP, Duo<OP>>(p, stream); break;
-    default: e = launch_tiles<OP, Small<OP>>(p, stream); break;
-  }
-  if (e != hipSuccess || p.splits == 1) return e;
-  const int N = OP == kForward ? p.F : p.K;
-  const int64_t rows = OP == kWeightGrad ? static_cast<int64_t>(p.G) * p.F : p.P;
-  const int64_t threads = rows * (N / 8) + (OP == kWeightGrad && p.db ? rows : 0);
-  const unsigned grid = static_cast<unsigned>((threads + 255) / 256);
-  switch (p.splits) {
-    case 2: product_join<OP, 2><<<grid, 256, 0, stream>>>(p); break;
-    case 4: product_join<OP, 4><<<grid, 256, 0, stream>>>(p); break;
-    case 8: product_join<OP, 8><<<grid, 256, 0, stream>>>(p); break;
-    default: return hipErrorInvalidValue;
-  }
-  return hipGetLastError();
-}
-
 }  // namespace
+
+hipError_t launch_forward(const ProductArgs& p, int shape, hipStream_t stream) {
+  if (shape == kShapeThin8) return launch_thin<8>(p, stream);
+  if (shape == kShapeThin16) return launch_thin<16>(p, stream);
+  return launch_op<kForward>(p, shape, stream);
+}
 
 // Estimated microseconds of each shape: rounds of the GPU's tile slots times
 // contraction steps of 64.  A round whose tiles leave the second slot of the
@@ -571,19 +255,41 @@ size_t product_part_bytes(int op, int64_t P, int G, int K, int F, const ProductP
   return (rows * cols + (op == kWeightGrad ? rows : 0)) * 4 * plan.splits;
 }
 
-hipError_t launch_product(int op, const ProductArgs& p, const ProductPlan& plan,
-                          hipStream_t stream) {
+namespace {
+
+ProductArgs with_plan(int op, const ProductArgs& p, const ProductPlan& plan) {
   ProductArgs q = p;
   q.splits = plan.splits;
   q.cus = plan.cus;
-  if (op == kForward) return launch_op<kForward>(q, plan.shape, stream);
-  if (op == kInputGrad) return launch_op<kInputGrad>(q, plan.shape, stream);
-  // A weight gradient that will not stay in the 256 MB last-level cache is
-  // stored past the caches, which then keep the operands (1 GB of fp32: 389 us
-  // instead of 455; 185 MB: 346 instead of 336).
-  q.stream = static_cast<int64_t>(q.G) * q.F * q.K * (q.y_f32 ? 4 : 2) > (int64_t(256) << 20);
-  q.part_db = q.part + static_cast<int64_t>(q.splits) * q.G * q.F * q.K;
-  return launch_op<kWeightGrad>(q, plan.shape, stream);
+  if (op == kWeightGrad) {
+    // A weight gradient that will not stay in the 256 MB last-level cache is
+    // stored past the caches, which then keep the operands (1 GB of fp32: 389
+    // us instead of 455; 185 MB: 346 instead of 336).
+    q.stream = static_cast<int64_t>(q.G) * q.F * q.K * (q.y_f32 ? 4 : 2) > (int64_t(256) << 20);
+    q.part_db = q.part + static_cast<int64_t>(q.splits) * q.G * q.F * q.K;
+  }
+  return q;
+}
+
+}  // namespace
+
+hipError_t launch_product(int op, const ProductArgs& p, const ProductPlan& plan,
+                          hipStream_t stream) {
+  const ProductArgs q = with_plan(op, p, plan);
+  if (op == kForward) return launch_forward(q, plan.shape, stream);
+  if (op == kInputGrad) return launch_input_grad(q, plan.shape, stream);
+  return launch_weight_grad(q, plan.shape, stream);
+}
+
+hipError_t launch_gradients(const ProductArgs& x, const ProductPlan& px, const ProductArgs& w,
+                            const ProductPlan& pw, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  if (px.splits == 1 && pw.splits == 1 &&
+      launch_grad_pair(with_plan(kInputGrad, x, px), px.shape, with_plan(kWeightGrad, w, pw),
+                       pw.shape, stream, &e))
+    return e;
+  e = launch_product(kInputGrad, x, px, stream);
+  return e != hipSuccess ? e : launch_product(kWeightGrad, w, pw, stream);
 }
 
 hipError_t launch_source_rows(const int32_t* row_ids, int row_div, int64_t x_rows, int64_t P,

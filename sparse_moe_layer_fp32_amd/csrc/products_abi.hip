@@ -173,6 +173,27 @@ moe::ProductArgs map_args(const MapPlan& m, void* ws) {
   return p;
 }
 
+// The input and weight gradients that are wanted of p (with a = dy).
+hipError_t gradients(const MapPlan& m, const moe::ProductArgs& p, const uint16_t* w,
+                     const uint16_t* x, uint16_t* dx, void* dw, float* db, bool dw_f32,
+                     bool accumulate, const int32_t* src, int64_t x_rows, hipStream_t stream) {
+  moe::ProductArgs px = p, pw = p;
+  px.b = w;
+  px.y = dx;
+  pw.b = x;
+  pw.y = dw;
+  pw.y_f32 = dw_f32;
+  pw.accumulate = accumulate;
+  pw.db = db;
+  pw.src = src;
+  pw.x_rows = x_rows;
+  const bool want_w = dw || db;
+  if (dx && want_w) return moe::launch_gradients(px, m.dx, pw, m.dw, stream);
+  if (dx) return moe::launch_product(moe::kInputGrad, px, m.dx, stream);
+  if (want_w) return moe::launch_product(moe::kWeightGrad, pw, m.dw, stream);
+  return hipSuccess;
+}
+
 }  // namespace
 
 extern "C" {
@@ -230,23 +251,11 @@ moe_status moe_linear_backward(const moe_linear_config* cfg, const uint16_t* dy,
                      "activation gradient");
     p.a = dz;
   }
-  if (dx && cfg->tokens > 0) {
-    moe::ProductArgs q = p;
-    q.b = w;
-    q.y = dx;
-    MOE_CHECK_LAUNCH(moe::launch_product(moe::kInputGrad, q, m.dx, stream), "linear input gradient");
-  }
   // dbias with an activation is done above, except that nothing ran for 0 tokens
   float* db = act && cfg->tokens > 0 ? nullptr : dbias;
-  if (dw || db) {
-    p.b = x;
-    p.y = dw;
-    p.y_f32 = cfg->dw_dtype == MOE_DTYPE_F32;
-    p.accumulate = cfg->accumulate != 0;
-    p.db = db;
-    MOE_CHECK_LAUNCH(moe::launch_product(moe::kWeightGrad, p, m.dw, stream),
-                     "linear weight gradient");
-  }
+  MOE_CHECK_LAUNCH(gradients(m, p, w, x, cfg->tokens > 0 ? dx : nullptr, dw, db,
+                             cfg->dw_dtype == MOE_DTYPE_F32, cfg->accumulate != 0, nullptr, m.P, stream),
+                   "linear gradients");
   return ok();
 }
 
@@ -302,28 +311,15 @@ moe_status moe_grouped_backward(const moe_grouped_config* cfg, const uint16_t* d
   moe::ProductArgs p = map_args(m, ws);
   p.a = dy;
   p.offsets = offsets;
-  if (dx && cfg->rows > 0) {
-    moe::ProductArgs q = p;
-    q.b = w;
-    q.y = dx;
-    MOE_CHECK_LAUNCH(moe::launch_product(moe::kInputGrad, q, m.dx, stream), "grouped input gradient");
-  }
-  if (dw || dbias) {
-    if (dw && row_ids && cfg->rows > 0) {
-      int32_t* src = at<int32_t>(ws, m.src);
-      MOE_CHECK_LAUNCH(moe::launch_source_rows(row_ids, cfg->row_div, cfg->x_rows, m.P, src, stream),
-                       "source rows");
-      p.src = src;
-      p.x_rows = cfg->x_rows;
-    }
-    p.b = x;
-    p.y = dw;
-    p.y_f32 = cfg->dw_dtype == MOE_DTYPE_F32;
-    p.accumulate = cfg->accumulate != 0;
-    p.db = dbias;
-    MOE_CHECK_LAUNCH(moe::launch_product(moe::kWeightGrad, p, m.dw, stream),
-                     "grouped weight gradient");
-  }
+  const bool gather = dw && row_ids && cfg->rows > 0;
+  int32_t* src = gather ? at<int32_t>(ws, m.src) : nullptr;
+  if (gather)
+    MOE_CHECK_LAUNCH(moe::launch_source_rows(row_ids, cfg->row_div, cfg->x_rows, m.P, src, stream),
+                     "source rows");
+  MOE_CHECK_LAUNCH(gradients(m, p, w, x, cfg->rows > 0 ? dx : nullptr, dw, dbias,
+                             cfg->dw_dtype == MOE_DTYPE_F32, cfg->accumulate != 0, src,
+                             gather ? cfg->x_rows : m.P, stream),
+                   "grouped gradients");
   return ok();
 }
 
