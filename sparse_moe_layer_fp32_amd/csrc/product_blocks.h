@@ -279,12 +279,6 @@ int64_t tile_count(int op, int64_t P, int G, int K, int F, bool grouped, ShapeSi
   return (grouped ? P / s.bm + std::min<int64_t>(G, P) : (P + s.bm - 1) / s.bm) * nt;
 }
 
-// Slices of rows that the tiles of a Big launch's last round are cut into.
-int last_round_slices(int64_t units, int cus) {
-  const int64_t last = units % cus;
-  return last == 0 || last * 2 > cus ? 1 : last * 4 > cus ? 2 : 4;
-}
-
 template <int OP>
 unsigned block_count(const ProductArgs& p, int64_t units) {
   return static_cast<unsigned>(OP == kWeightGrad && p.offsets
@@ -299,16 +293,11 @@ unsigned grid_of(ProductArgs* p) {
       tile_count(OP, p->P, p->G, OP == kWeightGrad && !p->y ? 1 : p->K, p->F,
                  p->offsets != nullptr, {T::BM, T::BN}) * p->splits;
   p->whole = -1;
-  if (T::BM == 256 && T::BN == 256 && OP != kWeightGrad && !p->offsets && p->splits == 1) {
-    // Dense Big launches: tiles that would leave half of the GPU idle in the
-    // last round are cut into halves or quarters of their rows.
-    p->slices = last_round_slices(units, p->cus);
-    if (p->slices > 1) {
-      p->whole = static_cast<int>(units - units % p->cus);
-      const int64_t cut = p->whole / kNumXcd * kNumXcd;
-      return static_cast<unsigned>(
-          cut + ((units - cut) * p->slices + kNumXcd - 1) / kNumXcd * kNumXcd);
-    }
+  if (T::BM == 256 && T::BN == 256 && OP != kWeightGrad && !p->offsets && p->slices > 1) {
+    p->whole = static_cast<int>(units - units % p->cus);
+    const int64_t cut = p->whole / kNumXcd * kNumXcd;
+    return static_cast<unsigned>(
+        cut + ((units - cut) * p->slices + kNumXcd - 1) / kNumXcd * kNumXcd);
   }
   return block_count<OP>(*p, units);
 }
@@ -349,12 +338,12 @@ hipError_t launch_op(const ProductArgs& p, int shape, hipStream_t stream) {
 
 }  // namespace
 
-// Launches of one product in a shape, and of both gradients together (false:
-// these two shapes have no common launch).
+// Launches of one product in a shape, and of both gradients together (both
+// Small, or each Big or Half).
 hipError_t launch_forward(const ProductArgs& p, int shape, hipStream_t stream);
 hipError_t launch_input_grad(const ProductArgs& p, int shape, hipStream_t stream);
 hipError_t launch_weight_grad(const ProductArgs& p, int shape, hipStream_t stream);
-bool launch_grad_pair(const ProductArgs& x, int sx, const ProductArgs& w, int sw,
-                      hipStream_t stream, hipError_t* err);
+hipError_t launch_grad_pair(const ProductArgs& x, int sx, const ProductArgs& w, int sw,
+                            hipStream_t stream);
 
 }  // namespace moe

@@ -35,21 +35,14 @@ hipError_t launch_both(ProductArgs x, ProductArgs w, hipStream_t stream) {
 
 }  // namespace
 
-bool launch_grad_pair(const ProductArgs& x, int sx, const ProductArgs& w, int sw,
-                      hipStream_t stream, hipError_t* err) {
-  if (sx == kShapeSmall && sw == kShapeSmall)
-    *err = launch_both<Small<kInputGrad>, Small<kWeightGrad>>(x, w, stream);
-  else if (sx == kShapeBig && sw == kShapeBig)
-    *err = launch_both<Big<kInputGrad>, Big<kWeightGrad>>(x, w, stream);
-  else if (sx == kShapeBig && sw == kShapeHalf)
-    *err = launch_both<Big<kInputGrad>, Half<kWeightGrad>>(x, w, stream);
-  else if (sx == kShapeHalf && sw == kShapeBig)
-    *err = launch_both<Half<kInputGrad>, Big<kWeightGrad>>(x, w, stream);
-  else if (sx == kShapeHalf && sw == kShapeHalf)
-    *err = launch_both<Half<kInputGrad>, Half<kWeightGrad>>(x, w, stream);
-  else
-    return false;
-  return true;
+hipError_t launch_grad_pair(const ProductArgs& x, int sx, const ProductArgs& w, int sw,
+                            hipStream_t stream) {
+  if (sx == kShapeSmall) return launch_both<Small<kInputGrad>, Small<kWeightGrad>>(x, w, stream);
+  if (sx == kShapeBig)
+    return sw == kShapeBig ? launch_both<Big<kInputGrad>, Big<kWeightGrad>>(x, w, stream)
+                           : launch_both<Big<kInputGrad>, Half<kWeightGrad>>(x, w, stream);
+  return sw == kShapeBig ? launch_both<Half<kInputGrad>, Big<kWeightGrad>>(x, w, stream)
+                         : launch_both<Half<kInputGrad>, Half<kWeightGrad>>(x, w, stream);
 }
 
 }  // namespace moe

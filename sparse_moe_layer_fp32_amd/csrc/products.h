@@ -52,16 +52,20 @@ struct ProductArgs {
 struct ProductPlan {
   int shape;
   int splits;
-  int cus;  // compute units of the device
+  int cus;     // compute units of the device
+  int slices;  // Big: slices of rows that the last round's tiles are cut into
+  float us;    // its estimated time
 };
 ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus);
+// Plans of kInputGrad and kWeightGrad in one launch; false when two launches,
+// each by its own plan, are expected to be faster.
+bool pair_plan(int64_t P, int G, int K, int F, int cus, ProductPlan* x, ProductPlan* w);
 // Bytes of `part` (with part_db behind it) for that plan; 0 when splits == 1.
 size_t product_part_bytes(int op, int64_t P, int G, int K, int F, const ProductPlan& plan);
 hipError_t launch_product(int op, const ProductArgs& p, const ProductPlan& plan, hipStream_t stream);
-// kInputGrad of x and kWeightGrad of w, in one launch where their plans allow.
-// Split plans use their `part` in turn.
-hipError_t launch_gradients(const ProductArgs& x, const ProductPlan& px, const ProductArgs& w,
-                            const ProductPlan& pw, hipStream_t stream);
+// kInputGrad of x and kWeightGrad of w in one launch, by the plans of pair_plan.
+hipError_t launch_pair(const ProductArgs& x, const ProductPlan& px, const ProductArgs& w,
+                       const ProductPlan& pw, hipStream_t stream);
 
 // src[r] = row_ids[r] / row_div, or -1 where that is outside [0, x_rows); and
 // kSourcePad further entries of -1.

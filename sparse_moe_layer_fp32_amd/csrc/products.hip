@@ -190,62 +190,143 @@ constexpr ShapeCost kCosts[] = {{1, 1.66f, 0.83f, 9.5f},   // Big
                                 {2, 0.46f, 0.14f, 2.1f}};  // Small
 constexpr ShapeCost kFlatCost = {1, 0.62f, 0.42f, 5.0f};
 constexpr float kFilling = 0.93f;  // partly grows by this share up to one tile on every CU
+// Both gradients in one launch (383 backward passes, 64 to 16384 rows, 2e9 to
+// 6e11 operations, in each of ten pairs of shapes and apart: 2% slower than
+// the best measured on the mean; always apart would be 14% slower).
+constexpr float kSecondLaunch = 6.0f, kMixed = 1.08f, kLeftOver = 0.6f, kLongest = 0.85f;
 constexpr float kJoin = 2.4f, kJoinBytesPerUs = 7.65e6f;
 
-ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
-  const int64_t rows = op == kWeightGrad ? static_cast<int64_t>(G) * F : P;
-  const int64_t cols = op == kForward ? F : K;
+namespace {
+
+// A product's sizes as the estimates see them.
+struct Sizes {
+  int64_t rows, cols, steps;  // of the output, and contraction steps of 64
+  bool ragged;
+};
+
+Sizes sizes_of(int op, int64_t P, int G, int K, int F) {
   const int64_t L = op == kForward ? K : op == kInputGrad ? F : (P + G - 1) / G;
-  // Few rows a group: every shape streams the weights at HBM rate, Small a
-  // little faster (64 tokens on 8 of 288 experts, 4096 -> 1280: 235 us; Big
-  // 246, Half 243).
-  if (op != kWeightGrad && G > 1 && P > kThinRows && P <= 16 * static_cast<int64_t>(G))
-    return {kShapeSmall, 1, cus};
-  // Tiles as they will be, about: a group with rows has half a tile more (Big,
-  // whose launches give remainders smaller tiles: a quarter).
-  const bool ragged = G > 1;
-  auto tiles_of = [&](int s) {
-    int64_t n = tile_count(op, P, G, K, F, false, kShapeSizes[s]);
-    if (op != kWeightGrad && ragged)
-      n += (std::min<int64_t>(G, P) + 1) / (s == kShapeBig ? 4 : 2) *
-           ((cols + kShapeSizes[s].bn - 1) / kShapeSizes[s].bn);
-    return n;
-  };
-  const int64_t steps = std::max<int64_t>(1, (L + 63) / 64);
+  return {op == kWeightGrad ? static_cast<int64_t>(G) * F : P, op == kForward ? F : K,
+          std::max<int64_t>(1, (L + 63) / 64), G > 1};
+}
+
+// Tiles as they will be, about: a group with rows has half a tile more (Big,
+// whose launches give remainders smaller tiles: a quarter).
+int64_t tiles_about(int op, int64_t P, int G, int K, int F, int shape) {
+  const ShapeSize s = kShapeSizes[shape];
+  int64_t n = tile_count(op, P, G, K, F, false, s);
+  if (op != kWeightGrad && G > 1)
+    n += (std::min<int64_t>(G, P) + 1) / (shape == kShapeBig ? 4 : 2) *
+         (((op == kForward ? F : K) + s.bn - 1) / s.bn);
+  return n;
+}
+
+float partly_us(const ShapeCost& c, float steps, float taken) {
+  return steps * c.partly * (1.0f + kFilling * std::min(taken, 1.0f)) + c.fixed;
+}
+
+// Slices of rows that the tiles of a Big launch's last round are cut into:
+// tiles that would leave half of the GPU idle are halved or quartered (8192 x
+// 4096 -> 11264, 5.5 rounds: 606 us instead of 622).
+int last_round_slices(int64_t units, int cus) {
+  const int64_t last = units % cus;
+  return last == 0 || last * 2 > cus ? 1 : last * 4 > cus ? 2 : 4;
+}
+
+const ShapeCost& cost_of(int shape, int slices) {
+  return slices == 4 ? kFlatCost : kCosts[slices == 2 ? kShapeHalf : shape];
+}
+
+}  // namespace
+
+ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
+  const Sizes z = sizes_of(op, P, G, K, F);
   // Few rows: the thin kernel, while the rows of x, which every block reads,
   // weigh little (16 x 4096 -> 4096: 11.4 us against 13.8 for the best tile
   // and split; 16 x 11264 -> 4096: 27.6 against 23.8).
   if (op == kForward && P <= kThinRows && P * K <= 98304)
-    return {tiles_of(kShapeThin16) <= cus / 2 ? kShapeThin8 : kShapeThin16, 1, cus};
-  ProductPlan best{kShapeSmall, 1, cus};
+    return {tiles_about(op, P, G, K, F, kShapeThin16) <= cus / 2 ? kShapeThin8 : kShapeThin16, 1,
+            cus, 1};
+  // Few rows a group: every shape streams the weights at HBM rate, Small a
+  // little faster (64 tokens on 8 of 288 experts, 4096 -> 1280: 235 us; Big
+  // 246, Half 243).
+  if (op != kWeightGrad && z.ragged && P > kThinRows && P <= 16 * static_cast<int64_t>(G))
+    return {kShapeSmall, 1, cus, 1};
+  ProductPlan best{kShapeSmall, 1, cus, 1};
   float best_us = 0.0f;
   for (int s = kShapeBig; s <= kShapeSmall; ++s) {
     const ShapeCost& c = kCosts[s];
-    const int64_t tiles = tiles_of(s), slots = static_cast<int64_t>(cus) * c.per_cu;
-    for (int splits = 1; splits <= 8 && splits <= steps; splits *= 2) {
+    const int64_t tiles = tiles_about(op, P, G, K, F, s);
+    const int64_t slots = static_cast<int64_t>(cus) * c.per_cu;
+    for (int splits = 1; splits <= 8 && splits <= z.steps; splits *= 2) {
       const int64_t units = tiles * splits, rest = units % slots;
-      const float n = static_cast<float>((steps + splits - 1) / splits);
-      float us = static_cast<float>(units / slots) * (n * c.full + c.fixed);
-      if (ragged && units > slots)  // tiles of different lengths end at different times
-        us = static_cast<float>(units) / slots * (n * c.full + c.fixed);
+      const float n = static_cast<float>((z.steps + splits - 1) / splits);
+      const float whole = n * c.full + c.fixed;
+      const int slices = s == kShapeBig && op != kWeightGrad && !z.ragged && splits == 1
+                             ? last_round_slices(units, cus)
+                             : 1;
+      float us = static_cast<float>(units / slots) * whole;
+      if (z.ragged && units > slots)  // tiles of different lengths end at different times
+        us = static_cast<float>(units) / slots * whole;
       else if (rest > cus)
-        us += n * c.full + c.fixed;
-      else if (rest) {
-        const int slices = s == kShapeBig && op != kWeightGrad && !ragged && splits == 1
-                               ? last_round_slices(units, cus)
-                               : 1;
-        const ShapeCost& l = slices == 4 ? kFlatCost : slices == 2 ? kCosts[kShapeHalf] : c;
-        us += n * l.partly * (1.0f + kFilling * static_cast<float>(rest * slices) / cus) + l.fixed;
-      }
+        us += whole;
+      else if (rest)
+        us += partly_us(cost_of(s, slices), n, static_cast<float>(rest * slices) / cus);
       if (splits > 1)
-        us += kJoin + static_cast<float>(rows) * cols * (8.0f * splits + 4.0f) / kJoinBytesPerUs;
+        us += kJoin + static_cast<float>(z.rows) * z.cols * (8.0f * splits + 4.0f) / kJoinBytesPerUs;
       if (best_us == 0.0f || us < best_us) {
         best_us = us;
-        best = {s, splits, cus};
+        best = {s, splits, cus, slices, us};
       }
     }
   }
   return best;
+}
+
+bool pair_plan(int64_t P, int G, int K, int F, int cus, ProductPlan* x, ProductPlan* w) {
+  const Sizes zx = sizes_of(kInputGrad, P, G, K, F), zw = sizes_of(kWeightGrad, P, G, K, F);
+  const ProductPlan ax = product_plan(kInputGrad, P, G, K, F, cus);
+  const ProductPlan aw = product_plan(kWeightGrad, P, G, K, F, cus);
+  float best_us = ax.us + aw.us + kSecondLaunch;
+  bool found = false;
+  auto consider = [&](int sx, int slices, int sw) {
+    const ShapeCost &cx = cost_of(sx, slices), &cw = kCosts[sw];
+    const float slots = static_cast<float>(cus) * cw.per_cu;
+    const float nx = static_cast<float>(tiles_about(kInputGrad, P, G, K, F, sx) * slices);
+    const float nw = static_cast<float>(tiles_about(kWeightGrad, P, G, K, F, sw));
+    const float lx = static_cast<float>(zx.steps), lw = static_cast<float>(zw.steps);
+    float us;
+    if (nx + nw <= cus) {  // one round
+      const float taken = (nx + nw) / cus;
+      us = std::max(partly_us(cx, lx, taken), partly_us(cw, lw, taken));
+    } else {
+      // as much of the GPU's time as the tiles take, and of the last round
+      // what a tile leaves over
+      const float tx = lx * cx.full + cx.fixed, tw = lw * cw.full + cw.fixed;
+      const float rounds = (nx + nw) / slots;
+      const float last = rounds - static_cast<float>(static_cast<int>(rounds));
+      us = std::max((nx * tx + nw * tw) / slots * kMixed +
+                        (last > 0.0f ? (1.0f - last) * tw * kLeftOver : 0.0f),
+                    std::max(tx, tw) * kLongest);
+    }
+    if (us < best_us) {
+      best_us = us;
+      found = true;
+      *x = {sx, 1, cus, slices};
+      *w = {sw, 1, cus, 1};
+    }
+  };
+  for (int sw : {kShapeBig, kShapeHalf}) {
+    consider(kShapeHalf, 1, sw);
+    consider(kShapeBig, 1, sw);
+    // (a cut tile's slices take the place of whole tiles in the last round only)
+    if (!zx.ragged && tiles_about(kInputGrad, P, G, K, F, kShapeBig) < cus) {
+      consider(kShapeBig, 2, sw);
+      consider(kShapeBig, 4, sw);
+    }
+  }
+  consider(kShapeSmall, 1, kShapeSmall);
+  return found;
 }
 
 size_t product_part_bytes(int op, int64_t P, int G, int K, int F, const ProductPlan& plan) {
@@ -261,6 +342,7 @@ ProductArgs with_plan(int op, const ProductArgs& p, const ProductPlan& plan) {
   ProductArgs q = p;
   q.splits = plan.splits;
   q.cus = plan.cus;
+  q.slices = plan.slices;
   if (op == kWeightGrad) {
     // A weight gradient that will not stay in the 256 MB last-level cache is
     // stored past the caches, which then keep the operands (1 GB of fp32: 389
@@ -281,15 +363,10 @@ hipError_t launch_product(int op, const ProductArgs& p, const ProductPlan& plan,
   return launch_weight_grad(q, plan.shape, stream);
 }
 
-hipError_t launch_gradients(const ProductArgs& x, const ProductPlan& px, const ProductArgs& w,
-                            const ProductPlan& pw, hipStream_t stream) {
-  hipError_t e = hipSuccess;
-  if (px.splits == 1 && pw.splits == 1 &&
-      launch_grad_pair(with_plan(kInputGrad, x, px), px.shape, with_plan(kWeightGrad, w, pw),
-                       pw.shape, stream, &e))
-    return e;
-  e = launch_product(kInputGrad, x, px, stream);
-  return e != hipSuccess ? e : launch_product(kWeightGrad, w, pw, stream);
+hipError_t launch_pair(const ProductArgs& x, const ProductPlan& px, const ProductArgs& w,
+                       const ProductPlan& pw, hipStream_t stream) {
+  return launch_grad_pair(with_plan(kInputGrad, x, px), px.shape, with_plan(kWeightGrad, w, pw),
+                          pw.shape, stream);
 }
 
 hipError_t launch_source_rows(const int32_t* row_ids, int row_div, int64_t x_rows, int64_t P,

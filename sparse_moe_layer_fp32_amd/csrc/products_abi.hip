@@ -188,10 +188,13 @@ hipError_t gradients(const MapPlan& m, const moe::ProductArgs& p, const uint16_t
   pw.src = src;
   pw.x_rows = x_rows;
   const bool want_w = dw || db;
-  if (dx && want_w) return moe::launch_gradients(px, m.dx, pw, m.dw, stream);
-  if (dx) return moe::launch_product(moe::kInputGrad, px, m.dx, stream);
-  if (want_w) return moe::launch_product(moe::kWeightGrad, pw, m.dw, stream);
-  return hipSuccess;
+  moe::ProductPlan plan_x, plan_w;
+  if (dx && dw && moe::pair_plan(m.P, m.G, m.K, m.F, m.dx.cus, &plan_x, &plan_w))
+    return moe::launch_pair(px, plan_x, pw, plan_w, stream);
+  hipError_t e = hipSuccess;
+  if (dx) e = moe::launch_product(moe::kInputGrad, px, m.dx, stream);
+  if (e == hipSuccess && want_w) e = moe::launch_product(moe::kWeightGrad, pw, m.dw, stream);
+  return e;
 }
 
 }  // namespace
