@@ -408,6 +408,71 @@ def test_grouped_backward_optional_results(moe, want):
     check_grouped_backward(moe, GROUPS["tile_edges"], 72, 136, want=want, seed=6)
 
 
+def test_grouped_beyond_32_bits(moe):
+    """Weights, rows and results whose element and byte offsets pass 2^32: the
+    first and last groups and rows against the definition."""
+    E, K, F, P = 520, 8192, 1032, 540_000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    normal = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda").normal_(generator=g)  # noqa: E731
+    x, w, dy = normal(P, K), normal(E, F, K), normal(P, F)
+    assert x.numel() > 2 ** 32 and w.numel() > 2 ** 32
+    sizes = [70, 130] + [0] * (E - 4) + [P - 500, 300]
+    off = torch.tensor([0] + list(itertools.accumulate(sizes)), dtype=torch.int32, device="cuda")
+    cfg = moe.make_grouped_config(P, E, K, F)
+    ws = moe.alloc_grouped_workspace(cfg)
+    y = torch.empty(P, F, dtype=torch.bfloat16, device="cuda")
+    moe.moe_grouped_forward(cfg, x, None, off, w, None, y, ws)
+    dx = torch.empty(P, K, dtype=torch.bfloat16, device="cuda")
+    dw = torch.full((E, F, K), 3.0, device="cuda")
+    moe.moe_grouped_backward(cfg, dy, x, None, off, w, dx, dw, None, ws)
+    torch.cuda.synchronize()
+    last = P - 300
+    for e, i, j in ((0, 0, 70), (1, 70, 200), (E - 2, last - 90, last), (E - 1, last, P)):
+        xe, we, de = x[i:j].double(), w[e].double(), dy[i:j].double()
+        want, mag = xe @ we.t(), xe.abs() @ we.abs().t()
+        within(y[i:j], want, 1.01 * sum_err(K, mag) + pu.BF16_HALF * want.abs(), f"y of group {e}")
+        want, mag = de @ we, de.abs() @ we.abs()
+        within(dx[i:j], want, 1.01 * sum_err(F, mag) + pu.BF16_HALF * want.abs(), f"dx {e}")
+        if e != E - 2:
+            within(dw[e], de.t() @ xe, sum_err(j - i, de.abs().t() @ xe.abs()) + 1e-30, f"dw {e}")
+    assert (dw[2:E - 2] == 0).all()
+
+
+def test_binding_refuses_what_a_kernel_would_misread(moe):
+    """Sizes, types, layouts and missing tensors, refused before any launch."""
+    z = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d, device="cuda")  # noqa: E731
+    cfg = moe.make_linear_config(8, 64, 72)
+    ws = moe.alloc_linear_workspace(cfg)
+    ok = dict(x=z(8, 64), w=z(72, 64), bias=z(72, d=torch.float32), residual=z(8, 72), y=z(8, 72))
+    call = lambda **kw: moe.moe_linear_forward(cfg, *{**ok, **kw}.values(), None, ws)  # noqa: E731
+    call()
+    for kw, err in ((dict(x=z(7, 64)), ValueError), (dict(w=z(64, 72)[:, :64]), ValueError),
+                    (dict(bias=z(72)), TypeError), (dict(y=z(8, 72, d=torch.float32)), TypeError),
+                    (dict(x=None), ValueError), (dict(x=z(64, 8).t()), ValueError),
+                    (dict(residual=z(8, 72).cpu()), ValueError), (dict(x=[1.0]), TypeError)):
+        with pytest.raises(err):
+            call(**kw)
+    with pytest.raises(ValueError):
+        moe.moe_linear_forward(cfg, *ok.values(), None, None)
+    with pytest.raises(moe.MoeError, match="workspace"):
+        moe.moe_linear_forward(cfg, *ok.values(), None, ws[:-256])
+    gc = moe.make_grouped_config(8, 3, 64, 72)
+    gws = moe.alloc_grouped_workspace(gc)
+    with pytest.raises(ValueError):  # offsets of two groups
+        moe.moe_grouped_forward(gc, z(8, 64), None, z(3, d=torch.int32), z(3, 72, 64), None,
+                                z(8, 72), gws)
+    with pytest.raises(TypeError):  # 64-bit offsets
+        moe.moe_grouped_forward(gc, z(8, 64), None, z(4, d=torch.int64), z(3, 72, 64), None,
+                                z(8, 72), gws)
+    sc = moe.make_swiglu_config(4, 64, ld=128)
+    gu_ = z(4, 128)
+    moe.moe_swiglu_forward(sc, gu_[:, :64], gu_[:, 64:], z(4, 64))
+    with pytest.raises(ValueError):  # another row stride
+        moe.moe_swiglu_forward(sc, z(4, 64), gu_[:, 64:], z(4, 64))
+    with pytest.raises(ValueError):
+        moe.moe_swiglu_forward(sc, gu_[:, ::2], gu_[:, 64:], z(4, 64))
+
+
 # ------------------------------------------------------------------ SwiGLU
 
 def swiglu_ref(g, u, limit):
