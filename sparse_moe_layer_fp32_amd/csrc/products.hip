@@ -305,7 +305,11 @@ bool pair_plan(int64_t P, int G, int K, int F, int cus, ProductPlan* x, ProductP
       const float tx = lx * cx.full + cx.fixed, tw = lw * cw.full + cw.fixed;
       const float rounds = (nx + nw) / slots;
       const float last = rounds - static_cast<float>(static_cast<int>(rounds));
-      us = std::max((nx * tx + nw * tw) / slots * kMixed +
+      // (long dense runs of Big tiles: one round saved; 8192 x 5120 -> 7168 997
+      // us, apart 1052)
+      const bool even = sx == kShapeBig && slices == 1 && sw == kShapeBig && rounds >= 2.0f &&
+                        !zx.ragged;
+      us = std::max((nx * tx + nw * tw) / slots * (even ? 0.98f : kMixed) +
                         (last > 0.0f ? (1.0f - last) * tw * kLeftOver : 0.0f),
                     std::max(tx, tw) * kLongest);
     }
