@@ -347,6 +347,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
   const bf16x8 ones{one, one, one, one, one, one, one, one};
 
   bf16x8 af[2][T::MB], bf[2][T::NB];
+  bf16x8 dbf[2][DBN];
   auto load_frags = [&](int kt, int ks, int set) MOE_INLINE {
     uint8_t* sa = aring + ((kt - k_first) % T::SA) * PA::BYTES;
     uint8_t* sb = bring + ((kt - k_first) % T::SB) * PB::BYTES;
@@ -354,12 +355,19 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
     for (int nb = 0; nb < T::NB; ++nb) bf[set][nb] = PB::frag(sb, bbase_l[nb], ks, lane);
 #pragma unroll
     for (int mb = 0; mb < T::MB; ++mb) af[set][mb] = PA::frag(sa, abase_l[mb], ks, lane);
+    if constexpr (DB)
+#pragma unroll
+      for (int i = 0; i < DBN; ++i) dbf[set][i] = PA::frag(sa, dbbase[i], ks, lane);
   };
-  auto barrier = [] { asm volatile("s_barrier" ::: "memory"); };
-  // Split rings (SA == 2 < SB): A is requested one step ahead, as a step
-  // starts, B SB - 1 steps ahead between the products.  Loads return in
-  // order, so when a step ends only the B stage requested in it may be in
-  // flight.  Equal rings: both are requested S - 1 steps ahead.
+  // The rings.  Step kt multiplies stage kt.  Before its last products, with
+  // all of the stage's fragments in registers, the waves wait for stage kt + 1
+  // and meet at a barrier, so that the first fragments of the next step load
+  // under these products and no step begins with empty registers.  After the
+  // barrier the slots of stage kt are free.  Split rings (SA == 2 < SB): A(kt +
+  // 2) is requested right there, B(kt + SB - 1) between the products before;
+  // loads return in order, so at the barrier only that B stage may be in
+  // flight.  Equal rings: both are requested S - 1 steps ahead between the
+  // products.
   constexpr bool SPLIT = T::SA != T::SB;
   constexpr int REFILLS = SPLIT ? T::JB : T::JA + T::JB;
   auto refill = [&](int kt, int d) MOE_INLINE {
@@ -370,12 +378,17 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
     else
       issue_b(kt + T::SB - 1, d - T::JA);
   };
-  auto step_end = [&](int kt) MOE_INLINE {
+  auto meet = [&](int kt) MOE_INLINE {
     if (kt + T::SB - 1 < k_last)
       wait_loads<(SPLIT ? T::JB : (T::SB - 2) * (T::JA + T::JB))>();
     else
       wait_loads<0>();
-    barrier();
+    // the wave's reads of stage kt have returned before another wave refills
+    // its slots
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (SPLIT && kt + 2 < k_last)
+#pragma unroll
+      for (int j = 0; j < T::JA; ++j) issue_a(kt + 2, j);
   };
   if (k_first < k_last) {
 #pragma unroll
@@ -394,58 +407,59 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
       wait_loads<(T::SB - 2) * (SPLIT ? T::JB : T::JA + T::JB)>();
     else
       wait_loads<0>();
-    barrier();
-    constexpr int MFMAS = T::KS * T::MB * T::NB;
-    constexpr int EVERY = MFMAS / REFILLS > 0 ? MFMAS / REFILLS : 1;
+    asm volatile("s_barrier" ::: "memory");
+    if (SPLIT && k_first + 1 < k_last)
+#pragma unroll
+      for (int j = 0; j < T::JA; ++j) issue_a(k_first + 1, j);
+    constexpr int EARLY = (T::KS - 1) * T::MB * T::NB;  // products before the barrier
+    constexpr int EVERY = EARLY / REFILLS > 0 ? EARLY / REFILLS : 1;
     const bool has_work = wm * (T::BM / T::WM) < un.rows && wn * (T::BN / T::WN) < cols;
     if (!has_work && !DB) {
       for (int kt = k_first; kt < k_last; ++kt) {
         use_ids();
         fetch_ids(kt + T::SB);
-        if (SPLIT && kt + 1 < k_last)
-#pragma unroll
-          for (int j = 0; j < T::JA; ++j) issue_a(kt + 1, j);
         if (kt + T::SB - 1 < k_last)
 #pragma unroll
           for (int d = 0; d < REFILLS; ++d) refill(kt, d);
-        if (kt + 1 < k_last) step_end(kt);
+        if (kt + 1 < k_last) meet(kt);
       }
     } else {
+      load_frags(k_first, 0, 0);
       auto step = [&](int kt, auto REFILL) MOE_INLINE {
         constexpr bool more = decltype(REFILL)::value;
         if (more) {
           use_ids();
           fetch_ids(kt + T::SB);
         }
-        if (SPLIT && kt + 1 < k_last)
-#pragma unroll
-          for (int j = 0; j < T::JA; ++j) issue_a(kt + 1, j);
-        load_frags(kt, 0, 0);
 #pragma unroll
         for (int ks = 0; ks < T::KS; ++ks) {
-          if (ks + 1 < T::KS) load_frags(kt, ks + 1, (ks + 1) & 1);
+          if (ks + 1 < T::KS) {
+            load_frags(kt, ks + 1, (ks + 1) & 1);
+          } else {
+            if (more && EARLY / EVERY < REFILLS)
+#pragma unroll
+              for (int d = EARLY / EVERY; d < REFILLS; ++d) refill(kt, d);
+            if (kt + 1 < k_last) {
+              meet(kt);
+              load_frags(kt + 1, 0, 0);
+            }
+          }
           if constexpr (DB)
 #pragma unroll
-            for (int i = 0; i < DBN; ++i)
-              dbacc[i] = mfma32(ones,
-                                PA::frag(aring + ((kt - k_first) % T::SA) * PA::BYTES, dbbase[i],
-                                         ks, lane),
-                                dbacc[i]);
+            for (int i = 0; i < DBN; ++i) dbacc[i] = mfma32(ones, dbf[ks & 1][i], dbacc[i]);
 #pragma unroll
           for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
             for (int nb = 0; nb < T::NB; ++nb) {
               acc[mb][nb] = mfma32(bf[ks & 1][nb], af[ks & 1][mb], acc[mb][nb]);
               const int i = (ks * T::MB + mb) * T::NB + nb;
-              if (more && i % EVERY == EVERY - 1 && i / EVERY < REFILLS) refill(kt, i / EVERY);
+              if (more && i < EARLY && i % EVERY == EVERY - 1 && i / EVERY < REFILLS)
+                refill(kt, i / EVERY);
             }
           __builtin_amdgcn_sched_barrier(0);
         }
-        if (more && MFMAS / EVERY < REFILLS)
-#pragma unroll
-          for (int d = MFMAS / EVERY; d < REFILLS; ++d) refill(kt, d);
-        if (kt + 1 < k_last) step_end(kt);
       };
+      static_assert(T::KS % 2 == 0, "the next step's first fragments take set 0");
       int kt = k_first;
       for (; kt + T::SB - 1 < k_last; ++kt) step(kt, std::true_type{});
       for (; kt < k_last; ++kt) step(kt, std::false_type{});
