@@ -456,6 +456,18 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
               if (more && i < EARLY && i % EVERY == EVERY - 1 && i / EVERY < REFILLS)
                 refill(kt, i / EVERY);
             }
+          if constexpr (T::MB * T::NB == 8 && T::NW == 8) {
+            // Big: three fragment reads, then one after every two products
+            // (+1 to 1.5% on 8192 cubed; one after each product, or half of
+            // them first: +-0; the smaller tiles lose 2% to any such order).
+            __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+              __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+              __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
       };
