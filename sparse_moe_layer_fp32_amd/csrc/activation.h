@@ -17,22 +17,21 @@ __device__ __forceinline__ float sigmoid_fast(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * v));
 }
 
-// Phi(v) = erfc(-v / sqrt 2) / 2, the standard normal distribution function,
-// by Abramowitz and Stegun 7.1.26 (erfc(x) = t poly(t) e^(-x x) with
-// t = 1 / (1 + 0.3275911 x) for x >= 0, |error| <= 1.5e-7); *gauss gets
-// e^(-v v / 2).  The library erff takes about three times the instructions,
-// which the wide products' epilogues have no matrix work to hide behind.
-__device__ __forceinline__ float normal_cdf(float v, float* gauss) {
-  const float x = fabsf(v) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  const float e = __builtin_amdgcn_exp2f(-kLog2e * x * x);
+// 1 - Phi(|v|) = erfc(|v| / sqrt 2) / 2, the upper tail of the standard normal
+// distribution, by Abramowitz and Stegun 7.1.26 (erfc(x) = t poly(t) e^(-x x)
+// with t = 1 / (1 + 0.3275911 x), |error| <= 1.5e-7; here with the factors 1/2
+// and 1/sqrt 2 in the constants); *gauss gets e^(-v v / 2).  The library erff
+// takes about three times the instructions, which the wide products'
+// epilogues have no matrix work to hide behind.
+__device__ __forceinline__ float normal_tail(float v, float* gauss) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(v), 0.3275911f * 0.70710678118654752f, 1.0f));
+  float q = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+  q = fmaf(q, t, 0.5f * 1.421413741f);
+  q = fmaf(q, t, 0.5f * -0.284496736f);
+  q = fmaf(q, t, 0.5f * 0.254829592f);
+  const float e = __builtin_amdgcn_exp2f(v * v * (-0.5f * kLog2e));
   *gauss = e;
-  const float tail = 0.5f * q * t * e;
-  return v < 0.0f ? tail : 1.0f - tail;
+  return q * t * e;
 }
 
 constexpr float kGeluC = 0.79788456080286536f;  // sqrt(2 / pi)
@@ -42,9 +41,9 @@ __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
     case MOE_ACT_RELU:
       return v < 0.0f ? 0.0f : v;  // NaN stays
-    case MOE_ACT_GELU: {
-      float e;
-      return v * normal_cdf(v, &e);
+    case MOE_ACT_GELU: {  // v Phi(v) = max(v, 0) - |v| (1 - Phi(|v|)); |v| capped so that
+      float e;            // infinity times a tail of 0 stays 0
+      return fmaxf(v, 0.0f) - fminf(fabsf(v), 1e18f) * normal_tail(v, &e);
     }
     case MOE_ACT_GELU_TANH:  // v (1 + tanh(q)) / 2 = v sigmoid(2 q)
       return v * sigmoid_fast(2.0f * kGeluC * v * fmaf(kGeluA * v, v, 1.0f));
@@ -61,8 +60,8 @@ __device__ __forceinline__ float act_slope(float v, int act) {
       return v > 0.0f ? 1.0f : 0.0f;
     case MOE_ACT_GELU: {
       float e;
-      const float c = normal_cdf(v, &e);
-      return fmaf(v * 0.39894228040143268f, e, c);
+      const float tail = normal_tail(v, &e);
+      return fmaf(v * 0.39894228040143268f, e, v < 0.0f ? tail : 1.0f - tail);
     }
     case MOE_ACT_GELU_TANH: {
       const float s = sigmoid_fast(2.0f * kGeluC * v * fmaf(kGeluA * v, v, 1.0f));

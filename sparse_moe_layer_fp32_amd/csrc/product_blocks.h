@@ -17,19 +17,21 @@ __device__ __forceinline__ int clamp_row(int v, int64_t P) {
   return static_cast<int>(min<int64_t>(max(v, 0), P));
 }
 
-// Block -> unit.  One group: each XCD takes a contiguous range (xcd_remap).
-// Ragged groups: runs of kRun units dealt over the XCDs in turn, since
-// contiguous ranges of experts of different sizes leave some XCDs long behind
-// the others.  Returns -1 for a block without work.
-constexpr int kRun = 16;
-__host__ __device__ __forceinline__ int64_t run_grid(int64_t units) {
-  return (units + kRun * kNumXcd - 1) / (kRun * kNumXcd) * (kRun * kNumXcd);
+// Block -> unit.  Forward, input gradient and one group: each XCD takes a
+// contiguous range (xcd_remap).  The weight gradient of ragged groups: runs of
+// units dealt over the XCDs in turn, since contiguous ranges of experts of
+// different sizes leave some XCDs long behind the others.  A run is a column
+// of up to 8 row tiles, whose blocks share x's panel in their L2, else 4 units
+// (48 experts of 1280 x 4096, five row tiles: runs of 5 375 us, 4 381, 16 409,
+// 1 459; 64 of 4096 x 2048, sixteen: runs of 4 410 us, 5 421, 10 438).
+// Returns -1 for a block without work.
+__host__ __device__ __forceinline__ int run_of(int F, int bm) {
+  const int tiles = (F + bm - 1) / bm;
+  return tiles >= 4 && tiles <= kGroupM ? tiles : 4;
 }
-template <int OP>
-__device__ __forceinline__ int unit_of_block(const ProductArgs& p, int bid, int nvalid) {
-  if (OP != kWeightGrad || !p.offsets) return xcd_remap(bid, nvalid);
+__device__ __forceinline__ int dealt_unit(int bid, int run, int nvalid) {
   const int xcd = bid % kNumXcd, slot = bid / kNumXcd;
-  const int u = (slot / kRun * kNumXcd + xcd) * kRun + slot % kRun;
+  const int u = (slot / run * kNumXcd + xcd) * run + slot % run;
   return u < nvalid ? u : -1;
 }
 
@@ -46,7 +48,8 @@ __device__ __forceinline__ bool find_unit(const ProductArgs& p, int bid, int* sh
   if constexpr (OP == kWeightGrad) {
     const int MT = (p.F + BM - 1) / BM;
     const int per = p.G * MT * NT;
-    const int u = unit_of_block<OP>(p, bid, per * p.splits);
+    const int u = p.offsets ? dealt_unit(bid, run_of(p.F, BM), per * p.splits)
+                            : xcd_remap(bid, per * p.splits);
     if (u < 0) return false;
     un->split = u / per;
     const int v = u % per;
@@ -90,7 +93,7 @@ __device__ __forceinline__ bool find_unit(const ProductArgs& p, int bid, int* sh
       total += sh[w];
     }
     total = __builtin_amdgcn_readfirstlane(total);
-    const int u = unit_of_block<OP>(p, bid, total * NT * p.splits);
+    const int u = xcd_remap(bid, total * NT * p.splits);
     if (u < 0) return false;
     int t = u % (total * NT) / NT;
     int at = before + incl - mine;
@@ -134,7 +137,7 @@ __device__ __forceinline__ bool find_unit(const ProductArgs& p, int bid, int* sh
       part = v % parts;
     }
   } else {
-    u = unit_of_block<OP>(p, bid, total * NT * p.splits);
+    u = xcd_remap(bid, total * NT * p.splits);
     if (u < 0) return false;
   }
   un->split = u / (total * NT);
@@ -279,11 +282,10 @@ int64_t tile_count(int op, int64_t P, int G, int K, int F, bool grouped, ShapeSi
   return (grouped ? P / s.bm + std::min<int64_t>(G, P) : (P + s.bm - 1) / s.bm) * nt;
 }
 
-template <int OP>
-unsigned block_count(const ProductArgs& p, int64_t units) {
-  return static_cast<unsigned>(OP == kWeightGrad && p.offsets
-                                   ? run_grid(units)
-                                   : (units + kNumXcd - 1) / kNumXcd * kNumXcd);
+// Blocks for that many units: whole rounds of the XCDs, of runs where they are dealt.
+unsigned block_count(int64_t units, int run) {
+  const int64_t round = static_cast<int64_t>(run) * kNumXcd;
+  return static_cast<unsigned>((units + round - 1) / round * round);
 }
 
 // The grid of a product in tiles of T, and the launch's own fields of p.
@@ -299,7 +301,7 @@ unsigned grid_of(ProductArgs* p) {
     return static_cast<unsigned>(
         cut + ((units - cut) * p->slices + kNumXcd - 1) / kNumXcd * kNumXcd);
   }
-  return block_count<OP>(*p, units);
+  return block_count(units, OP == kWeightGrad && p->offsets ? run_of(p->F, T::BM) : 1);
 }
 
 template <int OP, class T>

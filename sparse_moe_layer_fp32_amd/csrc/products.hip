@@ -160,7 +160,7 @@ hipError_t launch_thin(const ProductArgs& p, hipStream_t stream) {
   const int64_t units =
       tile_count(kForward, p.P, p.G, p.K, p.F, p.offsets != nullptr, {kThinRows, COLS});
   if (units <= 0) return hipSuccess;
-  const unsigned grid = block_count<kForward>(p, units);
+  const unsigned grid = block_count(units, 1);
   product_thin<COLS><<<grid, 64 * kThinWaves, 0, stream>>>(p);
   return hipGetLastError();
 }
