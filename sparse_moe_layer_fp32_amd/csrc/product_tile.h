@@ -230,9 +230,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
     astep = kStep * 2;
     if (OP == kForward && p.src) {
       abase = reinterpret_cast<const char*>(p.a);
-      } else {
+    } else {
       abase = reinterpret_cast<const char*>(p.a + static_cast<int64_t>(un.row0) * L);
-      }
+    }
     if (OP == kForward) {
       bbase = reinterpret_cast<const char*>(w + static_cast<int64_t>(un.col0) * L);
       bstep = kStep * 2;
