@@ -89,6 +89,7 @@ def test_linear_forward_activations(moe, T, K, F, act, y_dtype):
 @pytest.mark.parametrize("bias,residual,keep_z", itertools.product((False, True), repeat=3))
 def test_linear_forward_optional_operands(moe, bias, residual, keep_z):
     check_linear_forward(moe, 40, 136, 72, "gelu", "bf16", bias, residual, keep_z, seed=9)
+    check_linear_forward(moe, 700, 136, 2056, "silu", "f32", bias, residual, keep_z, seed=9)
 
 
 def check_linear_backward(moe, T, K, F, act="none", dw_dtype="f32", accumulate=False,
@@ -151,6 +152,14 @@ def test_linear_input_gradient_shapes(moe, T, K, F):
     (3000, 72, 2056), (2100, 72, 1032), (1500, 72, 72)])
 def test_linear_weight_gradient_shapes(moe, T, K, F):
     check_linear_backward(moe, T, K, F, want=("dw", "db"), seed=7)
+
+
+@pytest.mark.parametrize("T,K,F", [  # both in one launch, in each pair of shapes
+    (1000, 4104, 1032), (1000, 4104, 264), (4100, 2056, 2056), (700, 2056, 2056),
+    (300, 4104, 2056), (500, 4104, 1032), (700, 4104, 264), (300, 264, 264)])
+@pytest.mark.parametrize("accumulate,dw_dtype", [(False, "f32"), (True, "bf16")])
+def test_linear_both_gradients_shapes(moe, T, K, F, accumulate, dw_dtype):
+    check_linear_backward(moe, T, K, F, accumulate=accumulate, dw_dtype=dw_dtype, seed=7)
 
 
 @pytest.mark.parametrize("act", ("relu", "gelu", "gelu_tanh", "silu"))
@@ -302,6 +311,33 @@ def test_grouped_input_gradient_shapes(moe, sizes, K, F):
 def test_grouped_weight_gradient_shapes(moe, sizes, K, F, gather):
     check_grouped_backward(moe, sizes, K, F, before=3, after=70, gather=gather, want=("dw", "db"),
                            seed=7)
+
+
+@pytest.mark.parametrize("sizes,K,F", [  # both gradients in one launch
+    ([300, 0, 257, 73], 4104, 264), ([400, 1, 90, 0, 64, 65, 130, 190, 0], 2056, 264),
+    ([90, 0, 1, 64, 30, 0, 0, 5, 40], 2056, 264), ([90, 0, 1, 64, 30, 0, 0, 5, 40], 2056, 520),
+    ([150, 0, 1, 80], 264, 264)])
+@pytest.mark.parametrize("gather", (False, True))
+def test_grouped_both_gradients_shapes(moe, sizes, K, F, gather):
+    check_grouped_backward(moe, sizes, K, F, before=3, after=70, gather=gather, seed=7)
+
+
+def test_grouped_with_no_rows_of_x(moe):
+    """Every source lies outside an x of no rows: the products are zero."""
+    P, E, K, F = 40, 3, 72, 136
+    off = torch.tensor([0, 10, 10, 40], dtype=torch.int32, device="cuda")
+    ids = torch.arange(P, dtype=torch.int32, device="cuda")
+    x = torch.empty((0, K), dtype=torch.bfloat16, device="cuda")
+    w, dy = bf16(E, F, K).cuda(), bf16(P, F, seed=1).cuda()
+    b = f32(E, F, seed=2).cuda()
+    cfg = moe.make_grouped_config(P, E, K, F, x_rows=0, y_dtype="f32")
+    ws = moe.alloc_grouped_workspace(cfg)
+    y, dw = torch.empty(P, F, device="cuda"), torch.ones(E, F, K, device="cuda")
+    moe.moe_grouped_forward(cfg, x, ids, off, w, b, y, ws)
+    moe.moe_grouped_backward(cfg, dy, x, ids, off, None, None, dw, None, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(y[:10], b[0].expand(10, F)) and torch.equal(y[10:], b[2].expand(30, F))
+    assert (dw == 0).all()
 
 
 @pytest.mark.parametrize("accumulate", (False, True))
