@@ -409,23 +409,27 @@ class _Args:
     """Checks of one call's tensors, in the order cheapest for tensors that
     pass (a call of a few microseconds of GPU work spends as long here
     otherwise), and the errors for those that do not."""
-    __slots__ = ("device", "torch", "bf16", "f32", "i32")
+    __slots__ = ("device",)
+    torch = None  # with the types below, set at the first call
 
     def __init__(self):
-        torch = _torch()
-        self.torch = torch
+        if _Args.torch is None:
+            torch = _torch()
+            _Args.bf16 = (torch.bfloat16, torch.uint16, torch.int16)
+            _Args.f32, _Args.i32 = (torch.float32,), (torch.int32,)
+            _Args.Tensor = torch.Tensor
+            _Args.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            _Args.torch = torch
+        cuda = self.torch.cuda
         # -2: no tensor's device (a host tensor's is -1)
-        self.device = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
-        self.bf16 = (torch.bfloat16, torch.uint16, torch.int16)
-        self.f32 = (torch.float32,)
-        self.i32 = (torch.int32,)
+        self.device = cuda.current_device() if cuda.is_initialized() else -2
 
     def __call__(self, t, name, dtypes, numel, optional=False):
         """Device address of a contiguous tensor of `numel` elements on the
         current device."""
         if t is None and optional:
             return None
-        if (isinstance(t, self.torch.Tensor) and t.dtype in dtypes and t.numel() == numel
+        if (isinstance(t, self.Tensor) and t.dtype in dtypes and t.numel() == numel
                 and t.is_contiguous() and t.get_device() == self.device):
             return t.data_ptr()
         _ptr(t, dtypes, name)
@@ -437,11 +441,11 @@ class _Args:
         """Device address of a bf16 [rows][inter] tensor or view with the
         configuration's row stride."""
         ld = cfg.ld or cfg.inter
-        if (isinstance(t, self.torch.Tensor) and t.dtype in self.bf16
+        if (isinstance(t, self.Tensor) and t.dtype in self.bf16
                 and t.get_device() == self.device and t.shape == (cfg.rows, cfg.inter)
                 and (t.stride() == (ld, 1) or cfg.rows == 1 and t.stride(1) == 1)):
             return t.data_ptr()
-        if not isinstance(t, self.torch.Tensor):
+        if not isinstance(t, self.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.device.type != "cuda":
             raise ValueError(f"{name} must be on the GPU, got {t.device}")
@@ -461,16 +465,18 @@ class _Args:
         """(address, bytes) of a workspace tensor."""
         if ws is None:
             raise ValueError("ws is required")
-        n = ws.numel() if isinstance(ws, self.torch.Tensor) else 0
-        return self(ws, "ws", (getattr(ws, "dtype", None),), n), n * ws.element_size()
+        if (isinstance(ws, self.Tensor) and ws.is_contiguous()
+                and ws.get_device() == self.device):
+            return ws.data_ptr(), ws.nbytes
+        p = _ptr(ws, None, "ws")
+        self._elsewhere(ws, "ws")
+        return p, ws.nbytes
 
     def stream(self, stream):
         """The HIP stream: `stream`, or torch's current one (by its raw handle
         where torch gives it: a Stream object costs 2.5 us)."""
-        if stream is None:
-            raw = getattr(self.torch._C, "_cuda_getCurrentRawStream", None)
-            if raw is not None and self.device >= 0:
-                return raw(self.device)
+        if stream is None and self.raw_stream is not None and self.device >= 0:
+            return _Args.raw_stream(self.device)
         return _stream(stream)
 
     def _elsewhere(self, t, name):
