@@ -413,8 +413,8 @@ typedef struct {
 } moe_swiglu_config;
 
 /* h = SiLU(min(g, L)) * clamp(u, -L, L), the activation of moe_forward's
- * experts.  gate, up [rows] x ld bf16; h out [rows][I] bf16.  rows * ld is
- * below 2^35. */
+ * experts.  gate, up [rows] x ld bf16; h out [rows][I] bf16.  rows * ld is at
+ * most 2^35 - 2048. */
 moe_status moe_swiglu_forward(const moe_swiglu_config* cfg, const uint16_t* gate,
                               const uint16_t* up, uint16_t* h, hipStream_t stream);
 

@@ -156,8 +156,9 @@ moe_status validate_swiglu(const moe_swiglu_config* c, int64_t* ld) {
   if (c->inter % 8 || *ld % 8)
     return fail(MOE_ERR_UNSUPPORTED, "inter %d / row stride %d not multiples of 8", c->inter,
                 static_cast<int>(*ld));
-  if (c->rows >= kMaxElements / *ld)
-    return fail(MOE_ERR_UNSUPPORTED, "rows * row stride not below 2^35 elements");
+  // (a thread takes 8 elements, and a launch, in blocks of 256, holds fewer than 2^32 threads)
+  if (c->rows > (kMaxElements - 2048) / *ld)
+    return fail(MOE_ERR_UNSUPPORTED, "rows * row stride above 2^35 - 2048 elements");
   return MOE_OK;
 }
 

@@ -166,6 +166,14 @@ def test_swiglu_refuses_sizes(kw, status):
     assert lib.moe_swiglu_backward(ctypes.byref(cfg), *[FAKE] * 6, None) == status
 
 
+@pytest.mark.parametrize("rows,inter,ld", [
+    (2 ** 32 - 1, 8, 0), (2 ** 32 - 255, 8, 0), (2 ** 27 - 7, 256, 0), (2 ** 26 - 3, 256, 512)])
+def test_swiglu_refuses_more_threads_than_a_launch_holds(rows, inter, ld):
+    cfg, lib = swiglu(rows=rows, inter=inter, ld=ld), moe.load_library()
+    assert lib.moe_swiglu_forward(ctypes.byref(cfg), FAKE, FAKE, FAKE, None) == UNSUPPORTED
+    assert lib.moe_swiglu_backward(ctypes.byref(cfg), *[FAKE] * 6, None) == UNSUPPORTED
+
+
 def test_swiglu_refuses_pointers():
     cfg, lib = swiglu(), moe.load_library()
     for i in range(3):
