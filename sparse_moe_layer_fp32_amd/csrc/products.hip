@@ -92,35 +92,49 @@ __global__ __launch_bounds__(256) void source_rows_kernel(const int32_t* __restr
 }
 
 // dz = dy act'(z) and the column sums of each strip of rows: a block takes a
-// strip of 64 x 8 columns, its four waves every fourth row each, a thread
-// eight columns; the waves' sums meet in LDS.
+// strip of 64 x 8 columns, its waves rows in turn, a thread eight columns of
+// kStripAhead rows at a time, whose loads are under way together; the waves'
+// sums meet in LDS.  A single strip's sums are db itself.
 //
-// Bound: HBM, 6 bytes an element (4096 x 11264 with GELU and db: 49 us, 5.6
-// TB/s; with a quarter of the blocks, whose threads took 64 rows each, and a
-// column's strips summed by one thread, 110 us).
-constexpr int kStripWaves = 4, kStripCols = 64 * 8;
+// Bound: HBM, 6 bytes an element, and latency below some hundred blocks, where
+// more waves with fewer rows each help (GELU and db, both kernels, with 4, 8 and
+// 16 waves a block: 64 x 512 15.4, 9.1, 7.8 us; 1024 x 1024 20.6, 13.0, 11.4;
+// 4096 x 2048, 256 blocks, 25.6, 20.2, 18.5; 4096 x 4096, 512 blocks, 29.9, 27.9,
+// 29.9; 4096 x 11264 63.5, 59.6, 68.3; 65536 x 1280 114, 108, 120).
+constexpr int kStripAhead = 4, kStripCols = 64 * 8, kStripMany = 512;
 int strip_rows(int64_t T) { return 64 * static_cast<int>((T + 65535) / 65536); }
 
-__global__ __launch_bounds__(64 * kStripWaves) void act_grad_kernel(
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void act_grad_kernel(
     const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, int act, int64_t T, int F,
-    uint16_t* __restrict__ dz, float* __restrict__ part, int strip) {
-  __shared__ __attribute__((aligned(16))) float sums[kStripWaves - 1][kStripCols];
+    uint16_t* __restrict__ dz, float* __restrict__ part, int strip, int accumulate) {
+  __shared__ __attribute__((aligned(16))) float sums[WAVES - 1][kStripCols];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * kStripCols + lane * 8;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * strip;
   const int64_t r1 = min<int64_t>(T, r0 + strip);
   F8 sum{};
   if (c < F) {
-#pragma unroll 4
-    for (int64_t r = r0 + wave; r < r1; r += kStripWaves) {
-      F8 d = load8(dy + r * F + c);
-      const F8 v = load8(z + r * F + c);
+    for (int64_t r = r0 + wave; r < r1; r += WAVES * kStripAhead) {
+      u32x4 d4[kStripAhead], z4[kStripAhead];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        d.v[q] *= act_slope(v.v[q], act);
-        sum.v[q] += d.v[q];
+      for (int i = 0; i < kStripAhead; ++i) {
+        const int64_t at = min(r + i * WAVES, r1 - 1) * F + c;
+        d4[i] = *reinterpret_cast<const u32x4*>(dy + at);
+        z4[i] = *reinterpret_cast<const u32x4*>(z + at);
       }
-      store8(dz + r * F + c, d);
+#pragma unroll
+      for (int i = 0; i < kStripAhead; ++i) {
+        if (r + i * WAVES >= r1) break;
+        F8 d = unpack8(d4[i]);
+        const F8 v = unpack8(z4[i]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          d.v[q] *= act_slope(v.v[q], act);
+          sum.v[q] += d.v[q];
+        }
+        store8(dz + (r + i * WAVES) * F + c, d);
+      }
     }
   }
   if (!part) return;
@@ -128,12 +142,12 @@ __global__ __launch_bounds__(64 * kStripWaves) void act_grad_kernel(
   __syncthreads();
   if (wave > 0 || c >= F) return;
 #pragma unroll
-  for (int w = 0; w < kStripWaves - 1; ++w) {
+  for (int w = 0; w < WAVES - 1; ++w) {
     const F8 o = load8(&sums[w][lane * 8]);
 #pragma unroll
     for (int q = 0; q < 8; ++q) sum.v[q] += o.v[q];
   }
-  store8(part + static_cast<int64_t>(blockIdx.y) * F + c, sum);
+  put_grad8<false>(part + static_cast<int64_t>(blockIdx.y) * F + c, sum, accumulate);
 }
 
 // The strips' sums, in order: a block takes 64 columns, wave w every fourth strip.
@@ -390,10 +404,15 @@ hipError_t launch_act_grad(const uint16_t* dy, const uint16_t* z, int act, int64
                            hipStream_t stream) {
   const int rows = strip_rows(T), strips = static_cast<int>((T + rows - 1) / rows);
   const dim3 grid((F + kStripCols - 1) / kStripCols, strips);
-  act_grad_kernel<<<grid, 64 * kStripWaves, 0, stream>>>(dy, z, act, T, F, dz,
-                                                         db ? part : nullptr, rows);
+  const bool one = strips == 1;
+  float* const sums = !db ? nullptr : one ? db : part;
+  const bool add = one && accumulate;
+  if (static_cast<int64_t>(grid.x) * strips < kStripMany)
+    act_grad_kernel<16><<<grid, 64 * 16, 0, stream>>>(dy, z, act, T, F, dz, sums, rows, add);
+  else
+    act_grad_kernel<8><<<grid, 64 * 8, 0, stream>>>(dy, z, act, T, F, dz, sums, rows, add);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !db) return e;
+  if (e != hipSuccess || !db || one) return e;
   strip_sum_kernel<<<(F + 63) / 64, 256, 0, stream>>>(part, strips, F, db, accumulate);
   return hipGetLastError();
 }

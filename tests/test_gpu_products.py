@@ -174,6 +174,13 @@ def test_linear_backward_accumulates(moe, accumulate, dw_dtype, act):
     check_linear_backward(moe, 90, 200, 136, act, dw_dtype, accumulate, seed=4)
 
 
+@pytest.mark.parametrize("T,F", [  # one strip of rows, several, many blocks, strips of 128 rows
+    (1, 520), (17, 8), (64, 520), (65, 520), (1000, 264), (16400, 1032), (66000, 136)])
+@pytest.mark.parametrize("accumulate", (False, True))
+def test_linear_backward_strips_of_the_activation(moe, T, F, accumulate):
+    check_linear_backward(moe, T, 8, F, "silu", "f32", accumulate, want=("dw", "db"), seed=8)
+
+
 @pytest.mark.parametrize("want", [("dx",), ("dw",), ("db",), ("dx", "db"), ("dw", "db"), ()])
 @pytest.mark.parametrize("act", ("none", "gelu"))
 @pytest.mark.parametrize("T", (37, 2500))
