@@ -18,17 +18,25 @@ __device__ __forceinline__ float sigmoid_fast(float v) {
 }
 
 // 1 - Phi(|v|) = erfc(|v| / sqrt 2) / 2, the upper tail of the standard normal
-// distribution, by Abramowitz and Stegun 7.1.26 (erfc(x) = t poly(t) e^(-x x)
-// with t = 1 / (1 + 0.3275911 x), |error| <= 1.5e-7; here with the factors 1/2
-// and 1/sqrt 2 in the constants); *gauss gets e^(-v v / 2).  The library erff
-// takes about three times the instructions, which the wide products'
-// epilogues have no matrix work to hide behind.
+// distribution; *gauss gets e^(-v v / 2).  The tail is t poly(t) e^(-v v / 2)
+// with t = 1 / (1 + 0.305 |v|), where t poly(t) = erfcx(|v| / sqrt 2) / 2 was
+// fitted for its largest RELATIVE error over 0 <= |v| <= 13.5, 9.4e-8 (eight
+// terms; seven: 7.8e-7), since for v < 0 the tail alone is the value of GELU.
+// With fp32 roundings the tail is off by 5e-7 of itself up to |v| = 3 and by
+// 8e-6 at 13 (the exponent's rounding, v v / 2 times 2^-24 and more).  15
+// instructions; the library erfcf and the gaussian take 59, which the wide
+// products' epilogues have no matrix work to hide behind (8192 x 4096 -> 11264
+// with GELU: 658 us; 653 with the five terms of a formula for the absolute
+// error, 4.7e-4 off at v = -4 and 2e-2 at -10).
 __device__ __forceinline__ float normal_tail(float v, float* gauss) {
-  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(v), 0.3275911f * 0.70710678118654752f, 1.0f));
-  float q = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
-  q = fmaf(q, t, 0.5f * 1.421413741f);
-  q = fmaf(q, t, 0.5f * -0.284496736f);
-  q = fmaf(q, t, 0.5f * 0.254829592f);
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(v), 0.305f, 1.0f));
+  float q = fmaf(0.03669919f, t, -0.15298831f);
+  q = fmaf(q, t, 0.18571687f);
+  q = fmaf(q, t, -0.0379768f);
+  q = fmaf(q, t, 0.12102166f);
+  q = fmaf(q, t, 0.10342087f);
+  q = fmaf(q, t, 0.12246682f);
+  q = fmaf(q, t, 0.12163974f);
   const float e = __builtin_amdgcn_exp2f(v * v * (-0.5f * kLog2e));
   *gauss = e;
   return q * t * e;
