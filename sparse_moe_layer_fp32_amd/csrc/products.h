@@ -54,7 +54,7 @@ struct ProductPlan {
   int splits;
   int cus;     // compute units of the device
   int slices;  // Big: slices of rows that the last round's tiles are cut into
-  float us;    // its estimated time
+  float us;    // its estimated time (0 for a forward product of few rows)
 };
 ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus);
 // Plans of kInputGrad and kWeightGrad in one launch; false when two launches,

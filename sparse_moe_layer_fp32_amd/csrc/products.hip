@@ -253,45 +253,53 @@ const ShapeCost& cost_of(int shape, int slices) {
 
 }  // namespace
 
+namespace {
+
+// The estimate for `tiles` tiles of a shape in `splits` contraction ranges.
+float product_us(const Sizes& z, int64_t tiles, int shape, int splits, int slices, int cus) {
+  const ShapeCost& c = kCosts[shape];
+  const int64_t slots = static_cast<int64_t>(cus) * c.per_cu;
+  const int64_t units = tiles * splits, rest = units % slots;
+  const float n = static_cast<float>((z.steps + splits - 1) / splits);
+  const float whole = n * c.full + c.fixed;
+  float us = static_cast<float>(units / slots) * whole;
+  if (z.ragged && units > slots)  // tiles of different lengths end at different times
+    us = static_cast<float>(units) / slots * whole;
+  else if (rest > cus)
+    us += whole;
+  else if (rest)
+    us += partly_us(cost_of(shape, slices), n, static_cast<float>(rest * slices) / cus);
+  if (splits > 1)
+    us += kJoin + static_cast<float>(z.rows) * z.cols * (8.0f * splits + 4.0f) / kJoinBytesPerUs;
+  return us;
+}
+
+}  // namespace
+
 ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
   const Sizes z = sizes_of(op, P, G, K, F);
   // Few rows: the thin kernel, while the rows of x, which every block reads,
   // weigh little (16 x 4096 -> 4096: 11.4 us against 13.8 for the best tile
-  // and split; 16 x 11264 -> 4096: 27.6 against 23.8).
+  // and split; 16 x 11264 -> 4096: 27.6 against 23.8).  No estimate: only the
+  // gradients' are compared.
   if (op == kForward && P <= kThinRows && P * K <= 98304)
     return {tiles_about(op, P, G, K, F, kShapeThin16) <= cus / 2 ? kShapeThin8 : kShapeThin16, 1,
-            cus, 1};
+            cus, 1, 0.0f};
   // Few rows a group: every shape streams the weights at HBM rate, Small a
   // little faster (64 tokens on 8 of 288 experts, 4096 -> 1280: 235 us; Big
   // 246, Half 243).
   if (op != kWeightGrad && z.ragged && P > kThinRows && P <= 16 * static_cast<int64_t>(G))
-    return {kShapeSmall, 1, cus, 1};
-  ProductPlan best{kShapeSmall, 1, cus, 1};
-  float best_us = 0.0f;
+    return {kShapeSmall, 1, cus, 1,
+            product_us(z, tiles_about(op, P, G, K, F, kShapeSmall), kShapeSmall, 1, 1, cus)};
+  ProductPlan best{kShapeSmall, 1, cus, 1, 0.0f};
   for (int s = kShapeBig; s <= kShapeSmall; ++s) {
-    const ShapeCost& c = kCosts[s];
     const int64_t tiles = tiles_about(op, P, G, K, F, s);
-    const int64_t slots = static_cast<int64_t>(cus) * c.per_cu;
     for (int splits = 1; splits <= 8 && splits <= z.steps; splits *= 2) {
-      const int64_t units = tiles * splits, rest = units % slots;
-      const float n = static_cast<float>((z.steps + splits - 1) / splits);
-      const float whole = n * c.full + c.fixed;
       const int slices = s == kShapeBig && op != kWeightGrad && !z.ragged && splits == 1
-                             ? last_round_slices(units, cus)
+                             ? last_round_slices(tiles, cus)
                              : 1;
-      float us = static_cast<float>(units / slots) * whole;
-      if (z.ragged && units > slots)  // tiles of different lengths end at different times
-        us = static_cast<float>(units) / slots * whole;
-      else if (rest > cus)
-        us += whole;
-      else if (rest)
-        us += partly_us(cost_of(s, slices), n, static_cast<float>(rest * slices) / cus);
-      if (splits > 1)
-        us += kJoin + static_cast<float>(z.rows) * z.cols * (8.0f * splits + 4.0f) / kJoinBytesPerUs;
-      if (best_us == 0.0f || us < best_us) {
-        best_us = us;
-        best = {s, splits, cus, slices, us};
-      }
+      const float us = product_us(z, tiles, s, splits, slices, cus);
+      if (best.us == 0.0f || us < best.us) best = {s, splits, cus, slices, us};
     }
   }
   return best;

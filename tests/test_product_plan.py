@@ -1,0 +1,41 @@
+"""How the linear and grouped products are run: the choice of tile shape,
+contraction ranges, slices and shared launches (product_plan and pair_plan in
+csrc/products.hip, called as libmoe.so holds them, for an MI355X's 256 compute
+units; nothing is launched)."""
+import ctypes
+import itertools
+
+import pytest
+
+import sparse_moe_layer_fp32_amd as moe
+
+CUS = 256
+FORWARD, INPUT, WEIGHT = range(3)
+
+
+class Plan(ctypes.Structure):
+    _fields_ = [("shape", ctypes.c_int), ("splits", ctypes.c_int), ("cus", ctypes.c_int),
+                ("slices", ctypes.c_int), ("us", ctypes.c_float)]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    lib = moe.load_library()
+    plan = lib["_ZN3moe12product_planEiliiii"]
+    plan.argtypes = [ctypes.c_int, ctypes.c_int64] + [ctypes.c_int] * 4
+    plan.restype = Plan
+    pair = lib["_ZN3moe9pair_planEliiiiPNS_11ProductPlanES1_"]
+    pair.argtypes = [ctypes.c_int64] + [ctypes.c_int] * 4 + [ctypes.POINTER(Plan)] * 2
+    pair.restype = ctypes.c_bool
+    return plan, pair
+
+
+def test_every_gradient_has_an_estimated_time(lib):
+    """One launch for both gradients is weighed against the estimates of two:
+    none may be free."""
+    plan, _ = lib
+    for op, P, G, K, F in itertools.product(
+            (INPUT, WEIGHT), (1, 5, 16, 17, 40, 64, 200, 1000, 4608, 65536), (1, 2, 8, 64, 288),
+            (8, 64, 1280, 4096, 11264), (8, 200, 1024, 11264)):
+        p = plan(op, P, G, K, F, CUS)
+        assert p.us > 0 and p.splits >= 1, (op, P, G, K, F)
