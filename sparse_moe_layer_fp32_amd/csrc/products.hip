@@ -209,6 +209,7 @@ constexpr float kFilling = 0.93f;  // partly grows by this share up to one tile 
 // the best measured on the mean; always apart would be 14% slower).
 constexpr float kSecondLaunch = 6.0f, kMixed = 1.08f, kLeftOver = 0.6f, kLongest = 0.85f;
 constexpr float kJoin = 2.4f, kJoinBytesPerUs = 7.65e6f;
+constexpr float kRaggedJoin = 2.5f;  // more where each thread looks its group up
 
 namespace {
 
@@ -285,12 +286,21 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
   if (op == kForward && P <= kThinRows && P * K <= 98304)
     return {tiles_about(op, P, G, K, F, kShapeThin16) <= cus / 2 ? kShapeThin8 : kShapeThin16, 1,
             cus, 1, 0.0f};
-  // Few rows a group: every shape streams the weights at HBM rate, Small a
-  // little faster (64 tokens on 8 of 288 experts, 4096 -> 1280: 235 us; Big
-  // 246, Half 243).
-  if (op != kWeightGrad && z.ragged && P > kThinRows && P <= 16 * static_cast<int64_t>(G))
-    return {kShapeSmall, 1, cus, 1,
-            product_us(z, tiles_about(op, P, G, K, F, kShapeSmall), kShapeSmall, 1, 1, cus)};
+  // Few rows a group (at most a tile each, about): every shape streams the
+  // weights at HBM rate, Small a little faster (64 tokens on 8 of 288 experts,
+  // 4096 -> 1280: 235 us; Big 246, Half 243).  A few tiles of many steps are
+  // cut into ranges, one for every CU at most (17 rows in 8 groups, 11264 ->
+  // 256: 14 us in eight, 34 in one; 73 in 12, 2544 -> 480, 104 tiles of 40
+  // steps: 14 us in four, 11 in one).
+  if (op != kWeightGrad && z.ragged && P > kThinRows && P <= 16 * static_cast<int64_t>(G)) {
+    const int64_t tiles = tile_count(op, P, G, K, F, true, kShapeSizes[kShapeSmall]);
+    ProductPlan few{kShapeSmall, 1, cus, 1, product_us(z, tiles, kShapeSmall, 1, 1, cus)};
+    for (int splits = 2; splits <= 8 && splits <= z.steps && tiles * splits <= cus; splits *= 2) {
+      const float us = product_us(z, tiles, kShapeSmall, splits, 1, cus) + kRaggedJoin;
+      if (us < few.us) few = {kShapeSmall, splits, cus, 1, us};
+    }
+    return few;
+  }
   ProductPlan best{kShapeSmall, 1, cus, 1, 0.0f};
   for (int s = kShapeBig; s <= kShapeSmall; ++s) {
     const int64_t tiles = tiles_about(op, P, G, K, F, s);

@@ -712,3 +712,16 @@ def test_products_are_deterministic(moe):
         outs.append((dx, dw, db))
     for o in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+
+
+# ------------------------------------------------------------------ few groups, long contractions
+
+@pytest.mark.parametrize("sizes,K,F", [
+    ([9, 8], 4104, 72), ([0, 5, 0, 16, 1, 9, 0, 0], 2056, 136), ([40, 1, 0, 7], 8200, 64)])
+def test_grouped_few_rows_long_contraction(moe, sizes, K, F):
+    """Few rows a group and few tiles: the contraction is cut into ranges."""
+    for seed in (11, 12):
+        check_grouped_forward(moe, sizes, K, F, before=seed % 2, after=2, seed=seed,
+                              y_dtype=("bf16", "f32")[seed % 2])
+        check_grouped_backward(moe, sizes, F, K, before=seed % 2, after=2, want=("dx",), seed=seed)
+        check_grouped_backward(moe, sizes, F, K, seed=seed)

@@ -39,3 +39,13 @@ def test_every_gradient_has_an_estimated_time(lib):
             (8, 64, 1280, 4096, 11264), (8, 200, 1024, 11264)):
         p = plan(op, P, G, K, F, CUS)
         assert p.us > 0 and p.splits >= 1, (op, P, G, K, F)
+
+
+@pytest.mark.parametrize("op", (FORWARD, INPUT))
+@pytest.mark.parametrize("P,G,long,short", [
+    (17, 2, 11264, 64), (17, 8, 11264, 256), (40, 3, 4096, 64), (64, 16, 4096, 64),
+    (150, 10, 8192, 128)])
+def test_few_rows_a_group_split_a_long_contraction(lib, op, P, G, long, short):
+    """A handful of tiles of many steps each would leave the GPU idle."""
+    K, F = (long, short) if op == FORWARD else (short, long)
+    assert lib[0](op, P, G, K, F, CUS).splits >= 4
