@@ -1,0 +1,132 @@
+"""Long sums of the gradients, exactly: with entries of 1 and 2 in size every
+sum is a whole number below 2^24, so that fp32 in any order gives it exactly,
+and a row, a strip of rows or a contraction range that is lost, or taken
+twice, shows in every sum that it belongs to (the bounds of rounded sums grow
+faster with the rows than one row's share)."""
+import itertools
+
+import pytest
+import torch
+
+from tests import gpu_util as gu
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture
+def moe(request):
+    gu.note(f"[gpu-test] {request.node.nodeid}")
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import sparse_moe_layer_fp32_amd as m
+    m.load_library()
+    return m
+
+
+def whole(*shape, seed):
+    """-2, -1, 1 or 2."""
+    g = torch.Generator().manual_seed(seed)
+    v = torch.randint(0, 4, shape, generator=g, dtype=torch.int8)
+    return (v - 2 + (v >= 2)).to(torch.bfloat16)
+
+
+def case(T, K, F, relu, seed=0):
+    dy, x, z = whole(T, F, seed=seed), whole(T, K, seed=seed + 1), whole(T, F, seed=seed + 2)
+    return dy, x, z if relu else None
+
+
+def sums(dy, x, z):
+    """dw and db, exact in 64 bits."""
+    dz = dy.double() if z is None else dy.double() * (z > 0)
+    return dz.t() @ x.double(), dz.sum(0)
+
+
+# rows x in features -> out features, relu in front or none: strips of 64 and
+# 128 rows of the activation; one to 512 contraction ranges
+STRIPS = [(66000, 8, 136), (16400, 8, 1032), (1000, 8, 264), (65, 8, 520), (64, 8, 520)]
+RANGES = [(65536, 64, 64), (65537, 8, 8), (300_001, 8, 16), (16384, 256, 64), (40_000, 136, 72),
+          (66_000, 1032, 64), (70_000, 1288, 128), (9000, 72, 72), (9000, 264, 2056),
+          (9000, 520, 1032), (1500, 72, 72), (600, 8, 8), (5, 8, 8)]
+
+
+@pytest.mark.parametrize("T,K,F,relu", [(*s, True) for s in STRIPS] +
+                         [(*s, False) for s in RANGES if s[0] * s[2] < 3_000_000])
+def test_a_lost_row_or_strip_shows(T, K, F, relu):
+    """On the CPU, in the oracle: without one row, one strip or one range, or
+    with one taken twice, the sums differ."""
+    dy, x, z = case(T, K, F, relu)
+    dw, db = sums(dy, x, z)
+    assert dw.abs().max() < 2 ** 24 and db.abs().max() < 2 ** 24
+    for a, b in ((0, 1), (T - 1, T), (T // 2, T // 2 + 1), (T // 3, min(T, T // 3 + 64)),
+                 (T - T // 8, T), (0, max(1, T // 512))):
+        if a >= b:
+            continue
+        part = sums(dy[a:b], x[a:b], None if z is None else z[a:b])
+        lost_w, lost_b = (part[0] != 0).double().mean(), (part[1] != 0).double().mean()
+        assert lost_w > 0.3 and lost_b > 0.3, (a, b)  # of the elements change
+
+
+def run(moe, dy, x, z, accumulate=False, want=("dw", "db")):
+    T, F, K = dy.shape[0], dy.shape[1], x.shape[1]
+    cfg = moe.make_linear_config(T, K, F, activation="none" if z is None else "relu",
+                                 accumulate=accumulate)
+    ws = moe.alloc_linear_workspace(cfg)
+    ws.fill_(0xFF)
+    dw = torch.full((F, K), 3.0, device="cuda") if "dw" in want else None
+    db = torch.full((F,), 5.0, device="cuda") if "db" in want else None
+    dz = torch.empty(T, F, dtype=torch.bfloat16, device="cuda") if z is not None else None
+    moe.moe_linear_backward(cfg, dy, z, x if dw is not None else None, None, dz, None, dw, db, ws)
+    return dw, db
+
+
+@gpu
+@pytest.mark.parametrize("accumulate", (False, True))
+@pytest.mark.parametrize("T,K,F", STRIPS)
+def test_strips_of_the_activation(moe, T, K, F, accumulate):
+    dy, x, z = (t.cuda() for t in case(T, K, F, True))
+    want_w, want_b = sums(dy, x, z)
+    dw, db = run(moe, dy, x, z, accumulate)
+    assert torch.equal(dw.double(), want_w + 3 * accumulate)
+    assert torch.equal(db.double(), want_b + 5 * accumulate)
+
+
+@gpu
+@pytest.mark.parametrize("want", [("dw", "db"), ("db",), ("dw",)])
+@pytest.mark.parametrize("T,K,F", RANGES)
+def test_contraction_ranges(moe, T, K, F, want):
+    dy, x, _ = case(T, K, F, False)
+    dy, x = dy.cuda(), x.cuda()
+    want_w, want_b = sums(dy, x, None)
+    for accumulate in (False, True):
+        dw, db = run(moe, dy, x, None, accumulate, want)
+        assert dw is None or torch.equal(dw.double(), want_w + 3 * accumulate)
+        assert db is None or torch.equal(db.double(), want_b + 5 * accumulate)
+
+
+@gpu
+@pytest.mark.parametrize("gather", (False, True))
+@pytest.mark.parametrize("sizes,K,F", [
+    ([70_000, 3], 64, 64), ([0, 40_000, 0, 21_111], 72, 136), ([9000, 0, 1, 130, 64], 264, 72),
+    ([33_000], 8, 8)])
+def test_ragged_ranges(moe, sizes, K, F, gather):
+    before, after, per = 5, 9, 2
+    off = [before + s for s in itertools.accumulate(sizes, initial=0)]
+    P = off[-1] + after
+    dy, x = whole(P, F, seed=1).cuda(), whole(P, K, seed=2).cuda()
+    src, ids = torch.arange(P), None
+    if gather:
+        ids = torch.randperm(P, generator=torch.Generator().manual_seed(3)).to(torch.int32)
+        src = ids.long() // per
+    rows = x[src.cuda()].double()
+    dy[:before], dy[P - after:] = float("nan"), float("nan")
+    cfg = moe.make_grouped_config(P, len(sizes), K, F, x_rows=P, row_div=per if gather else 1)
+    ws = moe.alloc_grouped_workspace(cfg)
+    ws.fill_(0xFF)
+    dw = torch.full((len(sizes), F, K), 3.0, device="cuda")
+    db = torch.full((len(sizes), F), 5.0, device="cuda")
+    moe.moe_grouped_backward(cfg, dy, x, ids.cuda() if gather else None,
+                             torch.tensor(off, dtype=torch.int32, device="cuda"), None, None, dw,
+                             db, ws)
+    for e, (i, j) in enumerate(zip(off, off[1:])):
+        d = dy[i:j].double()
+        assert torch.equal(dw[e].double(), d.t() @ rows[i:j]), e
+        assert torch.equal(db[e].double(), d.sum(0)), e
