@@ -262,6 +262,50 @@ __global__ __launch_bounds__(256) void product_join(ProductArgs p) {
   }
 }
 
+// The same for a weight gradient in more than eight ranges.  A thread takes
+// eight consecutive values of an eighth of the ranges, in order and
+// kJoinAhead loads at a time; the eighths' sums meet in LDS, in order too.
+// The values of dW come first, then db's.
+constexpr int kJoinItems = 32, kJoinParts = 8, kJoinAhead = 8;
+
+__global__ __launch_bounds__(kJoinItems * kJoinParts) void product_join_many(ProductArgs p) {
+  __shared__ __attribute__((aligned(16))) float sums[kJoinParts - 1][kJoinItems * 8];
+  const int64_t rows = static_cast<int64_t>(p.G) * p.F;
+  const int64_t dw = p.y ? rows * p.K : 0, total = dw + (p.db ? rows : 0);
+  const int lane = threadIdx.x % kJoinItems, sub = threadIdx.x / kJoinItems;
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * kJoinItems + lane) * 8;
+  F8 v{};
+  if (at < total) {
+    const float* src = at < dw ? p.part + at : p.part_db + (at - dw);
+    const int64_t stride = at < dw ? dw : rows;
+    const int n = p.splits / kJoinParts;
+    src += sub * n * stride;
+    for (int s = 0; s < n; s += kJoinAhead) {
+      F8 w[kJoinAhead];
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i) w[i] = load8(src + min(s + i, n - 1) * stride);
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i)
+        if (s + i < n)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v.v[q] += w[i].v[q];
+    }
+  }
+  if (sub > 0) store8(&sums[sub - 1][lane * 8], v);
+  __syncthreads();
+  if (sub > 0 || at >= total) return;
+#pragma unroll
+  for (int i = 0; i < kJoinParts - 1; ++i) {
+    const F8 o = load8(&sums[i][lane * 8]);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v.v[q] += o.v[q];
+  }
+  if (at < dw)
+    put_grad8<false>(p, v, at);
+  else
+    put_grad8<false>(p.db + (at - dw), v, p.accumulate);
+}
+
 enum Shape : int {
   kShapeBig, kShapeHalf, kShapeDuo, kShapeSmall,
   kShapeThin8, kShapeThin16,  // forward only: product_thin
@@ -269,6 +313,8 @@ enum Shape : int {
 };
 
 constexpr int kThinRows = 16;  // rows of product_thin's tiles
+// Contraction ranges that product_join sums; a weight gradient may have more.
+constexpr int kFewSplits = 8;
 
 struct ShapeSize {
   int bm, bn;
@@ -326,6 +372,13 @@ hipError_t launch_op(const ProductArgs& p, int shape, hipStream_t stream) {
     default: e = launch_tiles<OP, Small<OP>>(p, stream); break;
   }
   if (e != hipSuccess || p.splits == 1) return e;
+  if (OP == kWeightGrad && p.splits > kFewSplits) {
+    const int64_t values = static_cast<int64_t>(p.G) * p.F * ((p.y ? p.K : 0) + (p.db ? 1 : 0));
+    const int64_t per = kJoinItems * 8;
+    product_join_many<<<static_cast<unsigned>((values + per - 1) / per),
+                        kJoinItems * kJoinParts, 0, stream>>>(p);
+    return hipGetLastError();
+  }
   const int N = OP == kForward ? p.F : p.K;
   const int64_t rows = OP == kWeightGrad ? static_cast<int64_t>(p.G) * p.F : p.P;
   const int64_t threads = rows * (N / 8) + (OP == kWeightGrad && p.db ? rows : 0);

@@ -209,6 +209,8 @@ constexpr float kFilling = 0.93f;  // partly grows by this share up to one tile 
 // the best measured on the mean; always apart would be 14% slower).
 constexpr float kSecondLaunch = 6.0f, kMixed = 1.08f, kLeftOver = 0.6f, kLongest = 0.85f;
 constexpr float kJoin = 2.4f, kJoinBytesPerUs = 7.65e6f;
+constexpr int kRangeSteps = 16;
+constexpr float kManyJoin = 2.0f;    // more in product_join_many
 constexpr float kRaggedJoin = 2.5f;  // more where each thread looks its group up
 
 namespace {
@@ -275,6 +277,18 @@ float product_us(const Sizes& z, int64_t tiles, int shape, int splits, int slice
   return us;
 }
 
+// Contraction ranges to consider.  A weight gradient's contraction, the rows,
+// may be much longer than its output has tiles: more than eight ranges where
+// eight leave a fifth of the CUs without work, while each has kRangeSteps
+// steps and a slot of the GPU (65536 x 64 -> 64, one tile: 64 ranges 11 us,
+// eight 35; 2^22 x 8 -> 8: 512 ranges 56 us, eight 1803; 76483 x 336 -> 264,
+// 30 tiles: 16 ranges 43 us, eight 40).
+int64_t most_splits(int op, const Sizes& z, int64_t tiles, int shape, int cus) {
+  const int64_t few = std::min<int64_t>(kFewSplits, z.steps);
+  if (op != kWeightGrad || tiles * kFewSplits * 5 > cus * 4) return few;
+  return std::max(few, std::min(z.steps / kRangeSteps, cus * kCosts[shape].per_cu / tiles));
+}
+
 }  // namespace
 
 ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
@@ -304,11 +318,12 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
   ProductPlan best{kShapeSmall, 1, cus, 1, 0.0f};
   for (int s = kShapeBig; s <= kShapeSmall; ++s) {
     const int64_t tiles = tiles_about(op, P, G, K, F, s);
-    for (int splits = 1; splits <= 8 && splits <= z.steps; splits *= 2) {
+    for (int splits = 1; splits <= most_splits(op, z, tiles, s, cus); splits *= 2) {
       const int slices = s == kShapeBig && op != kWeightGrad && !z.ragged && splits == 1
                              ? last_round_slices(tiles, cus)
                              : 1;
-      const float us = product_us(z, tiles, s, splits, slices, cus);
+      const float us = product_us(z, tiles, s, splits, slices, cus) +
+                       (splits > kFewSplits ? kManyJoin : 0.0f);
       if (best.us == 0.0f || us < best.us) best = {s, splits, cus, slices, us};
     }
   }

@@ -49,3 +49,14 @@ def test_few_rows_a_group_split_a_long_contraction(lib, op, P, G, long, short):
     """A handful of tiles of many steps each would leave the GPU idle."""
     K, F = (long, short) if op == FORWARD else (short, long)
     assert lib[0](op, P, G, K, F, CUS).splits >= 4
+
+
+@pytest.mark.parametrize("P,G,K,F", [(65536, 1, 64, 64), (1 << 22, 1, 8, 8), (66_000, 1, 8, 136),
+                                     (65536, 1, 1024, 64), (100_000, 4, 64, 128)])
+def test_long_narrow_weight_gradients_fill_the_gpu(lib, P, G, K, F):
+    """A contraction of many rows and an output of few tiles: more ranges, up
+    to a slot of the GPU each, and of at least 16 steps of 64 rows."""
+    p = lib[0](WEIGHT, P, G, K, F, CUS)
+    assert 8 < p.splits <= 512 and p.splits * 16 * 64 <= P // G + 63
+    for op in (FORWARD, INPUT):
+        assert lib[0](op, P, G, K, F, CUS).splits <= 8
