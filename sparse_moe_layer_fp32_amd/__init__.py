@@ -13,6 +13,9 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import itertools
+import math
+import operator
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -424,17 +427,22 @@ class _Args:
         # -2: no tensor's device (a host tensor's is -1)
         self.device = cuda.current_device() if cuda.is_initialized() else -2
 
-    def __call__(self, t, name, dtypes, numel, optional=False):
-        """Device address of a contiguous tensor of `numel` elements on the
-        current device."""
+    def __call__(self, t, name, dtypes, shape, optional=False):
+        """Device address of a contiguous tensor on the current device: of
+        `shape`, or the same memory in other dimensions, of which the last
+        ones together make up a row (heads of a row, batches of rows), or
+        flat."""
         if t is None and optional:
             return None
-        if (isinstance(t, self.Tensor) and t.dtype in dtypes and t.numel() == numel
+        if (isinstance(t, self.Tensor) and t.dtype in dtypes and t.shape == shape
                 and t.is_contiguous() and t.get_device() == self.device):
             return t.data_ptr()
         _ptr(t, dtypes, name)
+        numel, row = math.prod(shape), shape[-1]
         if t.numel() != numel:
             raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+        if t.dim() > 1 and row not in itertools.accumulate(reversed(t.shape), operator.mul):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected rows of {row}")
         return self._elsewhere(t, name)
 
     def rows(self, t, name, cfg):
@@ -508,9 +516,9 @@ def moe_linear_forward(cfg, x, w, bias, residual, y, z=None, ws=None, stream=Non
     a = _Args()
     bf = a.bf16
     _check(load_library().moe_linear_forward(
-        ctypes.byref(cfg), a(x, "x", bf, T * K), a(w, "w", bf, F * K),
-        a(bias, "bias", a.f32, F, True), a(residual, "residual", bf, T * F, True),
-        a(y, "y", a.of(cfg.y_dtype), T * F), a(z, "z", bf, T * F, True),
+        ctypes.byref(cfg), a(x, "x", bf, (T, K)), a(w, "w", bf, (F, K)),
+        a(bias, "bias", a.f32, (F,), True), a(residual, "residual", bf, (T, F), True),
+        a(y, "y", a.of(cfg.y_dtype), (T, F)), a(z, "z", bf, (T, F), True),
         *a.workspace(ws), a.stream(stream)))
 
 
@@ -522,10 +530,10 @@ def moe_linear_backward(cfg, dy, z, x, w, dz, dx, dw, dbias, ws=None, stream=Non
     bf = a.bf16
     plain = cfg.activation == 0
     _check(load_library().moe_linear_backward(
-        ctypes.byref(cfg), a(dy, "dy", bf, T * F), a(z, "z", bf, T * F, plain),
-        a(x, "x", bf, T * K, dw is None), a(w, "w", bf, F * K, dx is None),
-        a(dz, "dz", bf, T * F, plain), a(dx, "dx", bf, T * K, True),
-        a(dw, "dw", a.of(cfg.dw_dtype), F * K, True), a(dbias, "dbias", a.f32, F, True),
+        ctypes.byref(cfg), a(dy, "dy", bf, (T, F)), a(z, "z", bf, (T, F), plain),
+        a(x, "x", bf, (T, K), dw is None), a(w, "w", bf, (F, K), dx is None),
+        a(dz, "dz", bf, (T, F), plain), a(dx, "dx", bf, (T, K), True),
+        a(dw, "dw", a.of(cfg.dw_dtype), (F, K), True), a(dbias, "dbias", a.f32, (F,), True),
         *a.workspace(ws), a.stream(stream)))
 
 
@@ -547,9 +555,10 @@ def moe_grouped_forward(cfg, x, row_ids, offsets, w, bias, y, ws=None, stream=No
     a = _Args()
     bf = a.bf16
     _check(load_library().moe_grouped_forward(
-        ctypes.byref(cfg), a(x, "x", bf, cfg.x_rows * K), a(row_ids, "row_ids", a.i32, P, True),
-        a(offsets, "offsets", a.i32, E + 1), a(w, "w", bf, E * F * K),
-        a(bias, "bias", a.f32, E * F, True), a(y, "y", a.of(cfg.y_dtype), P * F),
+        ctypes.byref(cfg), a(x, "x", bf, (cfg.x_rows, K)),
+        a(row_ids, "row_ids", a.i32, (P,), True), a(offsets, "offsets", a.i32, (E + 1,)),
+        a(w, "w", bf, (E, F, K)), a(bias, "bias", a.f32, (E, F), True),
+        a(y, "y", a.of(cfg.y_dtype), (P, F)),
         *a.workspace(ws), a.stream(stream)))
 
 
@@ -559,10 +568,11 @@ def moe_grouped_backward(cfg, dy, x, row_ids, offsets, w, dx, dw, dbias, ws=None
     a = _Args()
     bf = a.bf16
     _check(load_library().moe_grouped_backward(
-        ctypes.byref(cfg), a(dy, "dy", bf, P * F), a(x, "x", bf, cfg.x_rows * K, dw is None),
-        a(row_ids, "row_ids", a.i32, P, True), a(offsets, "offsets", a.i32, E + 1),
-        a(w, "w", bf, E * F * K, dx is None), a(dx, "dx", bf, P * K, True),
-        a(dw, "dw", a.of(cfg.dw_dtype), E * F * K, True), a(dbias, "dbias", a.f32, E * F, True),
+        ctypes.byref(cfg), a(dy, "dy", bf, (P, F)), a(x, "x", bf, (cfg.x_rows, K), dw is None),
+        a(row_ids, "row_ids", a.i32, (P,), True), a(offsets, "offsets", a.i32, (E + 1,)),
+        a(w, "w", bf, (E, F, K), dx is None), a(dx, "dx", bf, (P, K), True),
+        a(dw, "dw", a.of(cfg.dw_dtype), (E, F, K), True),
+        a(dbias, "dbias", a.f32, (E, F), True),
         *a.workspace(ws), a.stream(stream)))
 
 
@@ -572,12 +582,12 @@ def moe_swiglu_forward(cfg, gate, up, h, stream=None):
     a = _Args()
     _check(load_library().moe_swiglu_forward(
         ctypes.byref(cfg), a.rows(gate, "gate", cfg), a.rows(up, "up", cfg),
-        a(h, "h", a.bf16, cfg.rows * cfg.inter), a.stream(stream)))
+        a(h, "h", a.bf16, (cfg.rows, cfg.inter)), a.stream(stream)))
 
 
 def moe_swiglu_backward(cfg, dh, gate, up, dgate, dup, h=None, stream=None):
     """dgate and dup for dh; h (may be None) is recomputed on the way."""
-    n = cfg.rows * cfg.inter
+    n = (cfg.rows, cfg.inter)
     a = _Args()
     _check(load_library().moe_swiglu_backward(
         ctypes.byref(cfg), a(dh, "dh", a.bf16, n), a.rows(gate, "gate", cfg),

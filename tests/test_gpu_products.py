@@ -725,3 +725,46 @@ def test_grouped_few_rows_long_contraction(moe, sizes, K, F):
                               y_dtype=("bf16", "f32")[seed % 2])
         check_grouped_backward(moe, sizes, F, K, before=seed % 2, after=2, want=("dx",), seed=seed)
         check_grouped_backward(moe, sizes, F, K, seed=seed)
+
+
+def test_binding_refuses_rows_of_another_length(moe):
+    """A transposed weight, and other tensors of the right size in rows of
+    another length; batched and flat tensors and rows in parts (heads) are the
+    same memory and pass."""
+    z = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d, device="cuda")  # noqa: E731
+    f = torch.float32
+    T, K, F, E = 8, 64, 72, 3
+    cfg = moe.make_linear_config(T, K, F, activation="relu")
+    ws = moe.alloc_linear_workspace(cfg)
+    fwd = dict(x=z(T, K), w=z(F, K), bias=z(F, d=f), residual=z(T, F), y=z(T, F), z=z(T, F))
+    bwd = dict(dy=z(T, F), z=z(T, F), x=z(T, K), w=z(F, K), dz=z(T, F), dx=z(T, K),
+               dw=z(F, K, d=f), dbias=z(F, d=f))
+    for call, ok in ((moe.moe_linear_forward, fwd), (moe.moe_linear_backward, bwd)):
+        call(cfg, *ok.values(), ws)
+        call(cfg, *[t.view(-1) for t in ok.values()], ws)
+        call(cfg, *[t.unflatten(0, (2, -1)) for t in ok.values()], ws)
+        call(cfg, *[t.unflatten(-1, (4, -1)) for t in ok.values()], ws)
+        for name, t in ok.items():
+            if t.dim() == 2:
+                with pytest.raises(ValueError, match=f"{name} has shape .*expected rows of"):
+                    call(cfg, *{**ok, name: t.view(t.shape[1], t.shape[0])}.values(), ws)
+    gc = moe.make_grouped_config(T, E, K, F)
+    gws = moe.alloc_grouped_workspace(gc)
+    off = z(E + 1, d=torch.int32)
+    gf = dict(x=z(T, K), row_ids=None, offsets=off, w=z(E, F, K), bias=z(E, F, d=f), y=z(T, F))
+    gb = dict(dy=z(T, F), x=z(T, K), row_ids=None, offsets=off, w=z(E, F, K), dx=z(T, K),
+              dw=z(E, F, K, d=f), dbias=z(E, F, d=f))
+    for call, ok in ((moe.moe_grouped_forward, gf), (moe.moe_grouped_backward, gb)):
+        call(gc, *ok.values(), gws)
+        for name, t in ok.items():
+            if name not in ("row_ids", "offsets"):
+                with pytest.raises(ValueError, match=f"{name} has shape .*expected rows of"):
+                    bad = t.transpose(-1, -2).contiguous()
+                    call(gc, *{**ok, name: bad}.values(), gws)
+    sc = moe.make_swiglu_config(T, K)
+    for call, n in ((moe.moe_swiglu_forward, 2), (moe.moe_swiglu_backward, 0)):
+        args = [z(T, K) for _ in range(3 if n else 6)]
+        call(sc, *args)
+        args[n] = z(K, T)
+        with pytest.raises(ValueError, match="expected rows of"):
+            call(sc, *args)
