@@ -29,10 +29,23 @@ __host__ __device__ __forceinline__ int run_of(int F, int bm) {
   const int tiles = (F + bm - 1) / bm;
   return tiles >= 4 && tiles <= kGroupM ? tiles : 4;
 }
-__device__ __forceinline__ int dealt_unit(int bid, int run, int nvalid) {
+__host__ __device__ __forceinline__ int dealt_unit(int bid, int run, int nvalid) {
   const int xcd = bid % kNumXcd, slot = bid / kNumXcd;
   const int u = (slot / run * kNumXcd + xcd) * run + slot % run;
   return u < nvalid ? u : -1;
+}
+
+// Block -> unit of a launch whose last tiles, from `cut` on (a multiple of the
+// XCDs), are cut into slices of rows: they follow the whole ones in every
+// XCD's order.  *part: which slice.
+__host__ __device__ __forceinline__ int cut_unit(int bid, int cut, int units, int slices,
+                                                 int* part) {
+  *part = 0;
+  if (bid < cut) return xcd_remap(bid, cut);
+  const int v = xcd_remap(bid - cut, (units - cut) * slices);
+  if (v < 0) return -1;
+  *part = v % slices;
+  return cut + v / slices;
 }
 
 // Block bid's unit, false if it has none.  Forward and input gradient: the
@@ -123,19 +136,10 @@ __device__ __forceinline__ bool find_unit(const ProductArgs& p, int bid, int* sh
   int part = 0, parts = 1;  // which of how many slices of the tile's rows
   int u;
   if (BM == 256 && p.whole >= 0) {
-    // the last tiles, cut into slices of rows, follow the whole ones in
-    // every XCD's order
-    parts = p.slices;
     const int cut = kNumXcd * (p.whole / kNumXcd);
-    if (bid < cut) {
-      u = xcd_remap(bid, cut);
-      parts = 1;
-    } else {
-      const int v = xcd_remap(bid - cut, (total * NT - cut) * parts);
-      if (v < 0) return false;
-      u = cut + v / parts;
-      part = v % parts;
-    }
+    u = cut_unit(bid, cut, total * NT, p.slices, &part);
+    if (u < 0) return false;
+    if (u >= cut) parts = p.slices;
   } else {
     u = xcd_remap(bid, total * NT * p.splits);
     if (u < 0) return false;

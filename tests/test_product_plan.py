@@ -4,13 +4,16 @@ csrc/products.hip, called as libmoe.so holds them, for an MI355X's 256 compute
 units; nothing is launched)."""
 import ctypes
 import itertools
+import math
+import random
 
 import pytest
 
 import sparse_moe_layer_fp32_amd as moe
+from tests.product_cases import (BIG, DUO, FORWARD, HALF, INPUT, PAIRS, SMALL, THIN8, THIN16, WAYS,
+                                 WEIGHT)
 
 CUS = 256
-FORWARD, INPUT, WEIGHT = range(3)
 
 
 class Plan(ctypes.Structure):
@@ -60,3 +63,76 @@ def test_long_narrow_weight_gradients_fill_the_gpu(lib, P, G, K, F):
     assert 8 < p.splits <= 512 and p.splits * 16 * 64 <= P // G + 63
     for op in (FORWARD, INPUT):
         assert lib[0](op, P, G, K, F, CUS).splits <= 8
+
+
+def ways(lib, op, P, G, K, F):
+    p = lib[0](op, P, G, K, F, CUS)
+    return p.shape, p.splits, p.slices
+
+
+def pair_ways(lib, P, G, K, F):
+    x, w = Plan(), Plan()
+    if not lib[1](P, G, K, F, CUS, x, w):
+        return None
+    assert x.splits == w.splits == w.slices == 1
+    return x.shape, x.slices, w.shape
+
+
+def test_the_table_of_sizes_takes_every_way(lib):
+    """tests/product_cases.py: each size is run as it says, and a sweep of
+    sizes finds no other way."""
+    for (op, ragged), rows in WAYS.items():
+        for shape, splits, slices, P, G, K, F in rows:
+            assert (G > 1) == ragged and ways(lib, op, P, G, K, F) == (shape, splits, slices), \
+                (op, P, G, K, F)
+    for sx, slices, sw, P, G, K, F in PAIRS:
+        assert pair_ways(lib, P, G, K, F) == (sx, slices, sw), (P, G, K, F)
+    known = {key: {row[:3] for row in rows} for key, rows in WAYS.items()}
+    pairs = {(row[4] > 1, row[:3]) for row in PAIRS}
+    r = random.Random(1)
+    size = lambda a, b: int(math.exp(r.uniform(math.log(a), math.log(b))))  # noqa: E731
+    for _ in range(40_000):
+        P, G, K, F = size(1, 1 << 18), r.choice((1, size(2, 300))), 8 * size(1, 1408), 8 * size(1, 1408)
+        for op in (FORWARD, INPUT, WEIGHT):
+            assert ways(lib, op, P, G, K, F) in known[op, G > 1], (op, P, G, K, F)
+        pair = pair_ways(lib, P, G, K, F)
+        assert pair is None or (G > 1, pair) in pairs, (P, G, K, F)
+
+
+def sizes_of(name):
+    """The sizes of a parametrised test in tests/test_gpu_products.py, as rows
+    and groups (with its rows of no group), in and out features."""
+    from tests import test_gpu_products as t
+    mark, = (m for m in getattr(t, name).pytestmark if m.name == "parametrize" and "K,F" in m.args[0])
+    for first, K, F in mark.args[1]:
+        yield (first, 1, K, F) if isinstance(first, int) else (sum(first) + 73, len(first), K, F)
+
+
+def test_sizes_of_the_shape_tests(lib):
+    """The sizes that the tests of tile shapes name still take those shapes."""
+    got = {name: [ways(lib, op, *s) for s in sizes_of(name)] for name, op in (
+        ("test_linear_forward_shapes", FORWARD), ("test_linear_input_gradient_shapes", INPUT),
+        ("test_linear_weight_gradient_shapes", WEIGHT), ("test_grouped_forward_shapes", FORWARD),
+        ("test_grouped_input_gradient_shapes", INPUT), ("test_grouped_weight_gradient_shapes", WEIGHT))}
+    assert got == {
+        "test_linear_forward_shapes": [
+            (BIG, 1, 2), (BIG, 1, 2), (BIG, 1, 4), (HALF, 1, 1), (HALF, 2, 1), (DUO, 1, 1),
+            (DUO, 4, 1), (SMALL, 2, 1), (SMALL, 4, 1), (SMALL, 8, 1)],
+        "test_linear_input_gradient_shapes": [
+            (BIG, 1, 2), (BIG, 1, 2), (BIG, 1, 4), (HALF, 1, 1), (HALF, 2, 1), (DUO, 1, 1),
+            (SMALL, 2, 1), (SMALL, 4, 1), (SMALL, 8, 1)],
+        "test_linear_weight_gradient_shapes": [
+            (BIG, 1, 1), (BIG, 4, 1), (DUO, 1, 1), (DUO, 4, 1), (DUO, 8, 1), (HALF, 1, 1),
+            (HALF, 2, 1), (HALF, 4, 1), (HALF, 8, 1), (SMALL, 2, 1), (SMALL, 4, 1), (SMALL, 8, 1)],
+        "test_grouped_forward_shapes": [(BIG, 1, 1), (DUO, 1, 1), (DUO, 1, 1), (SMALL, 4, 1)],
+        "test_grouped_input_gradient_shapes": [(BIG, 1, 1), (DUO, 1, 1), (HALF, 1, 1)],
+        "test_grouped_weight_gradient_shapes": [
+            (DUO, 1, 1), (HALF, 1, 1), (HALF, 2, 1), (SMALL, 8, 1), (SMALL, 2, 1)],
+    }
+    assert [pair_ways(lib, *s) for s in sizes_of("test_linear_both_gradients_shapes")] == [
+        (BIG, 1, BIG), (BIG, 1, HALF), (BIG, 2, HALF), (BIG, 4, BIG), (BIG, 4, HALF),
+        (HALF, 1, BIG), (HALF, 1, HALF), (SMALL, 1, SMALL)]
+    assert [pair_ways(lib, *s) for s in sizes_of("test_grouped_both_gradients_shapes")] == [
+        (BIG, 1, BIG), (BIG, 1, HALF), (HALF, 1, BIG), (HALF, 1, HALF), (SMALL, 1, SMALL)]
+    assert ways(lib, FORWARD, 1, 1, 4096, 1280)[0] == THIN8
+    assert ways(lib, FORWARD, 2, 1, 72, 4096)[0] == THIN16

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from tests import gpu_util as gu
+from tests.product_cases import FORWARD, INPUT, PAIRS, WAYS, WEIGHT
 
 gpu = pytest.mark.gpu
 
@@ -130,3 +131,75 @@ def test_ragged_ranges(moe, sizes, K, F, gather):
         d = dy[i:j].double()
         assert torch.equal(dw[e].double(), d.t() @ rows[i:j]), e
         assert torch.equal(db[e].double(), d.sum(0)), e
+
+
+def group_offsets(P, G, seed):
+    """G uneven groups, some of them empty, with rows of no group before and
+    behind them where there are enough."""
+    g = torch.Generator().manual_seed(seed)
+    cut = torch.randint(P // 16, P - P // 32 + 1, (G + 1,), generator=g).sort().values
+    return cut.to(torch.int32)
+
+
+def on_gpu(*shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    v = torch.randint(0, 4, shape, generator=g, dtype=torch.int8, device="cuda")
+    return (v - 2 + (v >= 2)).to(torch.bfloat16)
+
+
+def check_exactly(moe, P, G, K, F, want):
+    """The products named in `want` for P rows in G groups (1: the linear
+    map), against the same in 64 bits, bit for bit."""
+    x, w, dy = on_gpu(P, K, seed=1), on_gpu(G, F, K, seed=2), on_gpu(P, F, seed=3)
+    off = group_offsets(P, G, seed=P) if G > 1 else torch.tensor([0, P], dtype=torch.int32)
+    dev = off.cuda()
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    y = torch.full((P, F), 7.5, device="cuda") if FORWARD in want else None
+    dx = torch.full((P, K), 7.5, **bf) if INPUT in want else None
+    dw = torch.full((G, F, K), 7.5, device="cuda") if WEIGHT in want else None
+    db = torch.full((G, F), 7.5, device="cuda") if WEIGHT in want else None
+    if G > 1:
+        cfg = moe.make_grouped_config(P, G, K, F, y_dtype="f32")
+        ws = moe.alloc_grouped_workspace(cfg).fill_(0xFF)
+        if y is not None:
+            moe.moe_grouped_forward(cfg, x, None, dev, w, None, y, ws)
+        if dx is not None or dw is not None:
+            moe.moe_grouped_backward(cfg, dy, x, None, dev, w, dx, dw, db, ws)
+    else:
+        cfg = moe.make_linear_config(P, K, F, y_dtype="f32")
+        ws = moe.alloc_linear_workspace(cfg).fill_(0xFF)
+        if y is not None:
+            moe.moe_linear_forward(cfg, x, w[0], None, None, y, None, ws)
+        if dx is not None or dw is not None:
+            moe.moe_linear_backward(cfg, dy, None, x, w[0], None, dx, None if dw is None else dw[0],
+                                    None if db is None else db[0], ws)
+    seen = torch.zeros(P, dtype=torch.bool, device="cuda")
+    for e, (i, j) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        seen[i:j] = True
+        xe, we, de = x[i:j].double(), w[e].double(), dy[i:j].double()
+        if y is not None:
+            assert torch.equal(y[i:j].double(), xe @ we.t()), ("y", e)
+        if dx is not None:  # rounded once, to nearest even
+            assert torch.equal(dx[i:j], (de @ we).float().bfloat16()), ("dx", e)
+        if dw is not None:
+            assert torch.equal(dw[e].double(), de.t() @ xe), ("dw", e)
+            assert torch.equal(db[e].double(), de.sum(0)), ("db", e)
+    for t in (y, dx):
+        assert t is None or (t[~seen] == 7.5).all(), "a row of no group was written"
+
+
+@gpu
+@pytest.mark.parametrize("ragged", (False, True))
+@pytest.mark.parametrize("op", (FORWARD, INPUT, WEIGHT), ids=("forward", "input", "weight"))
+def test_every_way_to_run_a_product(moe, op, ragged):
+    """Tile shapes, contraction ranges and slices (tests/product_cases.py)."""
+    for case_ in WAYS[op, ragged]:
+        gu.note(f"  shape, ranges, slices, rows, groups, in, out: {case_}")
+        check_exactly(moe, *case_[3:], (op,))
+
+
+@gpu
+def test_every_way_to_run_both_gradients(moe):
+    for case_ in PAIRS:
+        gu.note(f"  dx shape, slices, dW shape, rows, groups, in, out: {case_}")
+        check_exactly(moe, *case_[3:], (INPUT, WEIGHT))
