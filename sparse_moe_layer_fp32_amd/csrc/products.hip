@@ -207,7 +207,8 @@ constexpr float kFilling = 0.93f;  // partly grows by this share up to one tile 
 // Both gradients in one launch (383 backward passes, 64 to 16384 rows, 2e9 to
 // 6e11 operations, in each of ten pairs of shapes and apart: 2% slower than
 // the best measured on the mean; always apart would be 14% slower).
-constexpr float kSecondLaunch = 6.0f, kMixed = 1.08f, kLeftOver = 0.6f, kLongest = 0.85f;
+constexpr float kSecondLaunch = 6.0f, kMixed = 1.08f, kLeftOver = 0.6f, kLongest = 0.85f,
+                kShared = 0.3f;
 constexpr float kJoin = 2.4f, kJoinBytesPerUs = 7.65e6f;
 constexpr int kRangeSteps = 16;
 constexpr float kManyJoin = 2.0f;    // more in product_join_many
@@ -359,6 +360,16 @@ bool pair_plan(int64_t P, int G, int K, int F, int cus, ProductPlan* x, ProductP
       us = std::max((nx * tx + nw * tw) / slots * (even ? 0.98f : kMixed) +
                         (last > 0.0f ? (1.0f - last) * tw * kLeftOver : 0.0f),
                     std::max(tx, tw) * kLongest);
+      // dW's blocks come behind dx's: its tiles start when dx's last ones do,
+      // and above a third of the CUs, about, two Small ones share one even then
+      // (11353 x 6152 -> 336, Half: 251 us, apart 178; 3800 x 728 -> 608, 120
+      // Small tiles of 60 steps: 38, apart 28; 2552 x 1360 -> 160, 66 of 40
+      // steps: 17, apart 21)
+      const int64_t slot = static_cast<int64_t>(slots), tiles = static_cast<int64_t>(nw);
+      const float rest = static_cast<float>(tiles % slot);
+      const bool shared = cw.per_cu > 1 && rest > kShared * cus;
+      const float end = rest == 0.0f ? 0.0f : shared ? tw : partly_us(cw, lw, rest / cus);
+      us = std::max(us, nx * tx / slots - tx + static_cast<float>(tiles / slot) * tw + end);
     }
     if (us < best_us) {
       best_us = us;

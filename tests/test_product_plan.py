@@ -136,3 +136,13 @@ def test_sizes_of_the_shape_tests(lib):
         (BIG, 1, BIG), (BIG, 1, HALF), (HALF, 1, BIG), (HALF, 1, HALF), (SMALL, 1, SMALL)]
     assert ways(lib, FORWARD, 1, 1, 4096, 1280)[0] == THIN8
     assert ways(lib, FORWARD, 2, 1, 72, 4096)[0] == THIN16
+
+
+def test_long_weight_gradients_run_apart(lib):
+    """A weight gradient of few long tiles does not queue behind the input
+    gradient's tiles in one launch; even and short ones do share it."""
+    for P, K, F in ((27930, 5616, 1000), (11353, 6152, 336), (45079, 1208, 5856), (3800, 728, 608),
+                    (4082, 648, 464), (9491, 8304, 440)):
+        assert pair_ways(lib, P, 1, K, F) is None, (P, K, F)
+    for P, K, F in ((8192, 5120, 7168), (4096, 4096, 11264), (2049, 4096, 1280), (1220, 1928, 1136)):
+        assert pair_ways(lib, P, 1, K, F) is not None, (P, K, F)
