@@ -203,3 +203,51 @@ def test_every_way_to_run_both_gradients(moe):
     for case_ in PAIRS:
         gu.note(f"  dx shape, slices, dW shape, rows, groups, in, out: {case_}")
         check_exactly(moe, *case_[3:], (INPUT, WEIGHT))
+
+
+@gpu
+@pytest.mark.parametrize("P,G,K,F", [
+    (3, 1, 65536, 8), (3, 1, 8, 65536), (300, 1, 65536, 16), (300, 1, 16, 65536), (40, 3, 65536, 8),
+    (40, 3, 8, 65536), (5000, 1024, 8, 24), (900, 1024, 136, 8), (1 << 22, 1024, 8, 8)])
+def test_ends_of_the_sizes(moe, P, G, K, F):
+    """The most features and the most groups."""
+    check_exactly(moe, P, G, K, F, (FORWARD, INPUT, WEIGHT))
+
+
+@gpu
+def test_the_most_rows(moe):
+    """2^26 rows; sums of entries of either sign stay below 2^24 on the way."""
+    T, K, F = 1 << 26, 8, 8
+    x, dy, z, w = (on_gpu(n, 8, seed=i) for i, n in enumerate((T, T, T, F)))
+    cfg = moe.make_linear_config(T, K, F, activation="relu", accumulate=True)
+    ws = moe.alloc_linear_workspace(cfg).fill_(0xFF)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    y, zz = torch.empty(T, F, **bf), torch.empty(T, F, **bf)
+    moe.moe_linear_forward(cfg, x, w, None, None, y, zz, ws)
+    dz, dx = torch.empty(T, F, **bf), torch.empty(T, K, **bf)
+    dw, db = torch.full((F, K), 3.0, device="cuda"), torch.full((F,), 5.0, device="cuda")
+    moe.moe_linear_backward(cfg, dy, z, x, w, dz, dx, dw, db, ws)
+    sw, sb = torch.full_like(dw, 3.0).double(), torch.full_like(db, 5.0).double()
+    for i in range(0, T, 1 << 22):
+        part = slice(i, i + (1 << 22))
+        xp, zp, dyp = x[part].double(), z[part], dy[part].double()
+        assert torch.equal(zz[part].double(), xp @ w.double().t())  # at most 32: exact in bf16
+        assert torch.equal(y[part].double(), (xp @ w.double().t()).clamp(min=0))
+        d = dyp * (zp > 0)
+        assert torch.equal(dz[part].double(), d)
+        assert torch.equal(dx[part].double(), d @ w.double())
+        sw, sb = sw + d.t() @ xp, sb + d.sum(0)
+    assert torch.equal(dw.double(), sw) and torch.equal(db.double(), sb)
+
+
+@gpu
+@pytest.mark.parametrize("T,K,F", [(40_000, 136, 72), (300_001, 8, 16), (600, 72, 72)])
+def test_bf16_gradients_of_many_ranges(moe, T, K, F):
+    """dw in bf16, added to what is there: rounded once, to nearest even."""
+    dy, x = on_gpu(T, F, seed=1), on_gpu(T, K, seed=2)
+    cfg = moe.make_linear_config(T, K, F, dw_dtype="bf16", accumulate=True)
+    dw = torch.full((F, K), 3.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_linear_backward(cfg, dy, None, x, None, None, None, dw, None,
+                            moe.alloc_linear_workspace(cfg).fill_(0xFF))
+    want = dy.double().t() @ x.double() + 3
+    assert torch.equal(dw, want.float().bfloat16())
