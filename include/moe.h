@@ -289,7 +289,9 @@ moe_status moe_dense_forward(const moe_dense_config* cfg, const uint16_t* x,
  * group sizes, SwiGLU between an expert's products, and the gradients of all
  * three.  A routed layer in training is moe_route, moe_permute, grouped gate
  * and up products of the gathered tokens, moe_swiglu_forward, and the grouped
- * down product; its backward pass is the same calls backwards.
+ * down product; the experts' backward pass is the same calls backwards, and
+ * the gradients of the combine and the router and the sum of dx over a token's
+ * rows are the caller's.
  *
  * Conventions and errors as above, and:
  *   - bf16 operands, exact products, fp32 accumulation; bias and its gradient
@@ -344,8 +346,10 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const uint16_t* x, c
  *   z      [T][F] bf16 as moe_linear_forward left it (not read, and may be
  *          NULL, with MOE_ACT_NONE)
  *   dz     out [T][F] bf16 (not written, and may be NULL, with MOE_ACT_NONE,
- *          where it is dy).  It is rounded to bf16 once, and dx and dw are
- *          formed from it as rounded; dbias sums the unrounded values.
+ *          where it is dy).  It is rounded to bf16 once, as an operand of
+ *          two matrix products has to be, and dx and dw are formed from it as
+ *          rounded: behind an activation an fp32 dw is as exact as a bf16 dz
+ *          (about 1.7e-3 in the 2-norm).  dbias sums the unrounded values.
  *   dx     out [T][K] bf16, or NULL;  dw out [F][K], dw_dtype, or NULL;
  *   dbias  out [F] fp32, or NULL
  * x is not read, and may be NULL, when dw is NULL; w likewise when dx is NULL.

@@ -100,7 +100,9 @@ __global__ __launch_bounds__(256) void source_rows_kernel(const int32_t* __restr
 // more waves with fewer rows each help (GELU and db, both kernels, with 4, 8 and
 // 16 waves a block: 64 x 512 15.4, 9.1, 7.8 us; 1024 x 1024 20.6, 13.0, 11.4;
 // 4096 x 2048, 256 blocks, 25.6, 20.2, 18.5; 4096 x 4096, 512 blocks, 29.9, 27.9,
-// 29.9; 4096 x 11264 63.5, 59.6, 68.3; 65536 x 1280 114, 108, 120).
+// 29.9; 8192 x 4096 51.9, 48.9, 53.2; 4096 x 11264 63.5, 59.6, 68.3; 65536 x 1280
+// 114, 108, 120).  Of four waves with one row each under way, 8192 x 4096 takes
+// 45.6, but 16384 x 4096 90.1 (here 85.4) and 4096 x 11264 62.4 (60.2).
 constexpr int kStripAhead = 4, kStripCols = 64 * 8, kStripMany = 512;
 int strip_rows(int64_t T) { return 64 * static_cast<int>((T + 65535) / 65536); }
 
@@ -206,7 +208,8 @@ constexpr ShapeCost kFlatCost = {1, 0.62f, 0.42f, 5.0f};
 constexpr float kFilling = 0.93f;  // partly grows by this share up to one tile on every CU
 // Both gradients in one launch (383 backward passes, 64 to 16384 rows, 2e9 to
 // 6e11 operations, in each of ten pairs of shapes and apart: 2% slower than
-// the best measured on the mean; always apart would be 14% slower).
+// the best measured on the mean; always apart would be 14% slower).  kShared
+// came later, from about 150 passes of up to 113000 rows.
 constexpr float kSecondLaunch = 6.0f, kMixed = 1.08f, kLeftOver = 0.6f, kLongest = 0.85f,
                 kShared = 0.3f;
 constexpr float kJoin = 2.4f, kJoinBytesPerUs = 7.65e6f;
@@ -353,8 +356,9 @@ bool pair_plan(int64_t P, int G, int K, int F, int cus, ProductPlan* x, ProductP
       const float tx = lx * cx.full + cx.fixed, tw = lw * cw.full + cw.fixed;
       const float rounds = (nx + nw) / slots;
       const float last = rounds - static_cast<float>(static_cast<int>(rounds));
-      // (long dense runs of Big tiles: one round saved; 8192 x 5120 -> 7168 997
-      // us, apart 1052)
+      // (long dense runs of Big tiles: one round saved; of thirteen sizes of 1e3
+      // to 15e3 rows none is slower than apart by more than 1%, and 8192 x 5120
+      // -> 7168 takes 943 us, apart 998, 1065 x 5960 -> 8248 219, apart 237)
       const bool even = sx == kShapeBig && slices == 1 && sw == kShapeBig && rounds >= 2.0f &&
                         !zx.ragged;
       us = std::max((nx * tx + nw * tw) / slots * (even ? 0.98f : kMixed) +
