@@ -322,7 +322,8 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
   ProductPlan best{kShapeSmall, 1, cus, 1, 0.0f};
   for (int s = kShapeBig; s <= kShapeSmall; ++s) {
     const int64_t tiles = tiles_about(op, P, G, K, F, s);
-    for (int splits = 1; splits <= most_splits(op, z, tiles, s, cus); splits *= 2) {
+    const int64_t most = most_splits(op, z, tiles, s, cus);
+    for (int splits = 1; splits <= most; splits *= 2) {
       const int slices = s == kShapeBig && op != kWeightGrad && !z.ragged && splits == 1
                              ? last_round_slices(tiles, cus)
                              : 1;
