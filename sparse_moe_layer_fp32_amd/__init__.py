@@ -112,6 +112,31 @@ def make_swiglu_config(rows, inter, ld=0, limit=0.0) -> moe_swiglu_config:
     return moe_swiglu_config(int(rows), int(inter), int(ld), float(limit), 0)
 
 
+class moe_dispatch_config(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("top_k", ctypes.c_int32),
+                ("hidden", ctypes.c_int32), ("token_dtype", ctypes.c_int32),
+                ("row_dtype", ctypes.c_int32)]
+
+
+def make_dispatch_config(tokens, rows, top_k, hidden, token_dtype="bf16",
+                         row_dtype="bf16") -> moe_dispatch_config:
+    """rows: rows of the experts' side (tokens * top_k when every pair has one)."""
+    return moe_dispatch_config(int(tokens), int(rows), int(top_k), int(hidden),
+                               _index(DTYPES, token_dtype, "token_dtype"),
+                               _index(DTYPES, row_dtype, "row_dtype"))
+
+
+class moe_quantize_config(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("top_k", ctypes.c_int32),
+                ("features", ctypes.c_int32)]
+
+
+def make_quantize_config(tokens, features, rows=None, top_k=1) -> moe_quantize_config:
+    """rows: rows of the codes (default: tokens)."""
+    return moe_quantize_config(int(tokens), int(tokens if rows is None else rows), int(top_k),
+                               int(features))
+
+
 _lib = None
 
 
@@ -154,10 +179,26 @@ def load_library():
     lib.moe_grouped_backward.argtypes = [gp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_swiglu_forward.argtypes = [sp, vp, vp, vp, vp]
     lib.moe_swiglu_backward.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp]
+    rp, qp = ctypes.POINTER(moe_dispatch_config), ctypes.POINTER(moe_quantize_config)
+    lib.moe_dispatch_forward.argtypes = [rp, vp, vp, vp, vp]
+    lib.moe_dispatch_backward.argtypes = [rp, vp, vp, vp, vp, vp]
+    lib.moe_combine_forward.argtypes = [rp, vp, vp, vp, vp, vp, vp]
+    lib.moe_combine_backward.argtypes = [rp, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_quantize_rows.argtypes = [qp, vp, vp, vp, vp, vp]
+    lib.moe_quantize_weight.argtypes = [ctypes.c_int32] * 3 + [vp, vp, vp, vp]
+    lib.moe_linear_fp8_workspace_size.argtypes = [lp]
+    lib.moe_linear_fp8_workspace_size.restype = sz
+    lib.moe_linear_forward_fp8.argtypes = [lp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_grouped_fp8_workspace_size.argtypes = [gp]
+    lib.moe_grouped_fp8_workspace_size.restype = sz
+    lib.moe_grouped_forward_fp8.argtypes = [gp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     for f in ("moe_route", "moe_permute", "moe_forward", "moe_forward_timed",
               "moe_workspace_view", "moe_dense_forward", "moe_forward_fp8", "moe_forward_fused",
               "moe_linear_forward", "moe_linear_backward", "moe_grouped_forward",
-              "moe_grouped_backward", "moe_swiglu_forward", "moe_swiglu_backward"):
+              "moe_grouped_backward", "moe_swiglu_forward", "moe_swiglu_backward",
+              "moe_dispatch_forward", "moe_dispatch_backward", "moe_combine_forward",
+              "moe_combine_backward", "moe_quantize_rows", "moe_quantize_weight",
+              "moe_linear_forward_fp8", "moe_grouped_forward_fp8"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -168,7 +209,11 @@ EXPORTED = ("moe_workspace_size", "moe_last_error", "moe_route", "moe_permute", 
             "moe_dense_forward", "moe_forward_fp8", "moe_forward_fused",
             "moe_forward_noalloc", "moe_linear_workspace_size", "moe_linear_forward",
             "moe_linear_backward", "moe_grouped_workspace_size", "moe_grouped_forward",
-            "moe_grouped_backward", "moe_swiglu_forward", "moe_swiglu_backward")
+            "moe_grouped_backward", "moe_swiglu_forward", "moe_swiglu_backward",
+            "moe_dispatch_forward", "moe_dispatch_backward", "moe_combine_forward",
+            "moe_combine_backward", "moe_quantize_rows", "moe_quantize_weight",
+            "moe_linear_fp8_workspace_size", "moe_linear_forward_fp8",
+            "moe_grouped_fp8_workspace_size", "moe_grouped_forward_fp8")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # MOE_NOALLOC_SCRATCH_BYTES
 
 
@@ -420,6 +465,7 @@ class _Args:
             torch = _torch()
             _Args.bf16 = (torch.bfloat16, torch.uint16, torch.int16)
             _Args.f32, _Args.i32 = (torch.float32,), (torch.int32,)
+            _Args.u8 = (torch.uint8, torch.float8_e4m3fn)
             _Args.Tensor = torch.Tensor
             _Args.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
             _Args.torch = torch
@@ -593,3 +639,131 @@ def moe_swiglu_backward(cfg, dh, gate, up, dgate, dup, h=None, stream=None):
         ctypes.byref(cfg), a(dh, "dh", a.bf16, n), a.rows(gate, "gate", cfg),
         a.rows(up, "up", cfg), a.rows(dgate, "dgate", cfg), a.rows(dup, "dup", cfg),
         a(h, "h", a.bf16, n, True), a.stream(stream)))
+
+
+# ------------------------------------------------------------------ rows out to the experts and back
+
+def moe_dispatch_forward(cfg, x, pair_pos, rows, stream=None):
+    """rows[pair_pos[t][j]] = x[t] for every pair whose position is a row."""
+    T, R, k, H = cfg.tokens, cfg.rows, cfg.top_k, cfg.hidden
+    a = _Args()
+    _check(load_library().moe_dispatch_forward(
+        ctypes.byref(cfg), a(x, "x", a.of(cfg.token_dtype), (T, H)),
+        a(pair_pos, "pair_pos", a.i32, (T, k)), a(rows, "rows", a.of(cfg.row_dtype), (R, H)),
+        a.stream(stream)))
+
+
+def moe_dispatch_backward(cfg, drows, pair_pos, base, dx, stream=None):
+    """dx[t] = base[t] + sum_j drows[pair_pos[t][j]] (base: may be None)."""
+    T, R, k, H = cfg.tokens, cfg.rows, cfg.top_k, cfg.hidden
+    a = _Args()
+    tok = a.of(cfg.token_dtype)
+    _check(load_library().moe_dispatch_backward(
+        ctypes.byref(cfg), a(drows, "drows", a.of(cfg.row_dtype), (R, H)),
+        a(pair_pos, "pair_pos", a.i32, (T, k)), a(base, "base", tok, (T, H), True),
+        a(dx, "dx", tok, (T, H)), a.stream(stream)))
+
+
+def moe_combine_forward(cfg, rows, pair_pos, weights, base, y, stream=None):
+    """y[t] = base[t] + sum_j weights[t][j] rows[pair_pos[t][j]] (weights, for
+    ones, and base: may be None)."""
+    T, R, k, H = cfg.tokens, cfg.rows, cfg.top_k, cfg.hidden
+    a = _Args()
+    tok = a.of(cfg.token_dtype)
+    _check(load_library().moe_combine_forward(
+        ctypes.byref(cfg), a(rows, "rows", a.of(cfg.row_dtype), (R, H)),
+        a(pair_pos, "pair_pos", a.i32, (T, k)), a(weights, "weights", a.f32, (T, k), True),
+        a(base, "base", tok, (T, H), True), a(y, "y", tok, (T, H)), a.stream(stream)))
+
+
+def moe_combine_backward(cfg, dy, rows, pair_pos, weights, drows, dweights, stream=None):
+    """drows[pair_pos[t][j]] = weights[t][j] dy[t] and dweights[t][j] = <dy[t],
+    rows[pair_pos[t][j]]> (each may be None; rows without dweights)."""
+    T, R, k, H = cfg.tokens, cfg.rows, cfg.top_k, cfg.hidden
+    a = _Args()
+    row = a.of(cfg.row_dtype)
+    _check(load_library().moe_combine_backward(
+        ctypes.byref(cfg), a(dy, "dy", a.of(cfg.token_dtype), (T, H)),
+        a(rows, "rows", row, (R, H), dweights is None), a(pair_pos, "pair_pos", a.i32, (T, k)),
+        a(weights, "weights", a.f32, (T, k), True), a(drows, "drows", row, (R, H), True),
+        a(dweights, "dweights", a.f32, (T, k), True), a.stream(stream)))
+
+
+# ------------------------------------------------------------------ products in 8 bits
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def moe_quantize_rows(cfg, x, pair_pos, codes, scales, stream=None):
+    """e4m3 codes and scales (a block of 128 columns each) of x's rows; with
+    pair_pos (else None), at the rows that it names."""
+    T, R, k, K = cfg.tokens, cfg.rows, cfg.top_k, cfg.features
+    a = _Args()
+    _check(load_library().moe_quantize_rows(
+        ctypes.byref(cfg), a(x, "x", a.bf16, (T, K)), a(pair_pos, "pair_pos", a.i32, (T, k), True),
+        a(codes, "codes", a.u8, (R, K)), a(scales, "scales", a.f32, (R, _blocks(K))),
+        a.stream(stream)))
+
+
+def moe_quantize_weight(w, codes, scales, stream=None):
+    """e4m3 codes and scales (a block of 128 x 128 each) of weights [F][K] or
+    [G][F][K]."""
+    a = _Args()
+    if not isinstance(w, a.Tensor) or w.dim() not in (2, 3):
+        raise ValueError("w must be a tensor of [F][K] or [G][F][K]")
+    F, K = w.shape[-2:]
+    G = w.shape[0] if w.dim() == 3 else 1
+    _check(load_library().moe_quantize_weight(
+        G, F, K, a(w, "w", a.bf16, tuple(w.shape)), a(codes, "codes", a.u8, tuple(w.shape)),
+        a(scales, "scales", a.f32, (G, _blocks(F), _blocks(K))), a.stream(stream)))
+
+
+def moe_linear_fp8_workspace_size(cfg: moe_linear_config) -> int:
+    n = load_library().moe_linear_fp8_workspace_size(ctypes.byref(cfg))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, moe_last_error())
+    return int(n)
+
+
+def alloc_linear_fp8_workspace(cfg: moe_linear_config, device=None):
+    return _alloc(moe_linear_fp8_workspace_size(cfg), device)
+
+
+def moe_linear_forward_fp8(cfg, x, x_scales, w, w_scales, bias, residual, y, z=None, ws=None,
+                           stream=None):
+    """moe_linear_forward of codes x and w with their scales."""
+    T, K, F = cfg.tokens, cfg.in_features, cfg.out_features
+    a = _Args()
+    _check(load_library().moe_linear_forward_fp8(
+        ctypes.byref(cfg), a(x, "x", a.u8, (T, K)), a(x_scales, "x_scales", a.f32, (T, _blocks(K))),
+        a(w, "w", a.u8, (F, K)), a(w_scales, "w_scales", a.f32, (_blocks(F), _blocks(K))),
+        a(bias, "bias", a.f32, (F,), True), a(residual, "residual", a.bf16, (T, F), True),
+        a(y, "y", a.of(cfg.y_dtype), (T, F)), a(z, "z", a.bf16, (T, F), True),
+        *a.workspace(ws), a.stream(stream)))
+
+
+def moe_grouped_fp8_workspace_size(cfg: moe_grouped_config) -> int:
+    n = load_library().moe_grouped_fp8_workspace_size(ctypes.byref(cfg))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, moe_last_error())
+    return int(n)
+
+
+def alloc_grouped_fp8_workspace(cfg: moe_grouped_config, device=None):
+    return _alloc(moe_grouped_fp8_workspace_size(cfg), device)
+
+
+def moe_grouped_forward_fp8(cfg, x, x_scales, row_ids, offsets, w, w_scales, bias, y, ws=None,
+                            stream=None):
+    """moe_grouped_forward of codes x and w with their scales."""
+    P, E, K, F = cfg.rows, cfg.num_groups, cfg.in_features, cfg.out_features
+    a = _Args()
+    _check(load_library().moe_grouped_forward_fp8(
+        ctypes.byref(cfg), a(x, "x", a.u8, (cfg.x_rows, K)),
+        a(x_scales, "x_scales", a.f32, (cfg.x_rows, _blocks(K))),
+        a(row_ids, "row_ids", a.i32, (P,), True), a(offsets, "offsets", a.i32, (E + 1,)),
+        a(w, "w", a.u8, (E, F, K)),
+        a(w_scales, "w_scales", a.f32, (E, _blocks(F), _blocks(K))),
+        a(bias, "bias", a.f32, (E, F), True), a(y, "y", a.of(cfg.y_dtype), (P, F)),
+        *a.workspace(ws), a.stream(stream)))

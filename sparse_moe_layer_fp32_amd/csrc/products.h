@@ -43,6 +43,14 @@ struct ProductArgs {
   int splits;
   float* part;
   float* part_db;
+  // e4m3 codes (forward): a and b as rows of K 16-bit pairs of codes, and their
+  // scales.  a's scale of row r and step s is a_scale[r a_scale_row + s
+  // a_scale_step], of x's row src(r) unless a_scale_ready, when it is of row r
+  // of y; b's are [G][F / 128][steps], rounded up.
+  const float* a_scale;
+  const float* b_scale;
+  int64_t a_scale_row, a_scale_step;
+  int a_scale_ready;
   // set by the launcher
   int cus;
   int whole, slices;  // Big tiles left whole (-1: all), slices of the rows of the others
@@ -60,6 +68,10 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus);
 // Plans of kInputGrad and kWeightGrad in one launch; false when two launches,
 // each by its own plan, are expected to be faster.
 bool pair_plan(int64_t P, int G, int K, int F, int cus, ProductPlan* x, ProductPlan* w);
+// The forward product of codes, with K in pairs of them; exact: fp32 results.
+ProductPlan product_fp8_plan(int64_t P, int G, int K, int F, int cus, bool exact);
+hipError_t launch_product_fp8(const ProductArgs& p, const ProductPlan& plan, bool exact,
+                              hipStream_t stream);
 // Bytes of `part` (with part_db behind it) for that plan; 0 when splits == 1.
 size_t product_part_bytes(int op, int64_t P, int G, int K, int F, const ProductPlan& plan);
 hipError_t launch_product(int op, const ProductArgs& p, const ProductPlan& plan, hipStream_t stream);

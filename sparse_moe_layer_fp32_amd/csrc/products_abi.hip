@@ -4,7 +4,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <initializer_list>
 
 #include "abi_util.h"
 #include "products.h"
@@ -12,8 +11,9 @@
 namespace {
 
 using moe::align_up;
-using moe::aligned16;
 using moe::at;
+using moe::check_pointers;
+using moe::check_workspace;
 using moe::fail;
 using moe::ok;
 
@@ -43,21 +43,6 @@ moe_status check_dtypes(int32_t y, int32_t dw) {
   for (int32_t t : {y, dw})
     if (t != MOE_DTYPE_BF16 && t != MOE_DTYPE_F32)
       return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", t);
-  return MOE_OK;
-}
-
-moe_status check_pointers(std::initializer_list<const void*> ptrs) {
-  for (const void* q : ptrs)
-    if (q && !aligned16(q)) return fail(MOE_ERR_UNSUPPORTED, "pointer %p not 16-byte aligned", q);
-  return MOE_OK;
-}
-
-moe_status check_workspace(size_t need, const void* ws, size_t ws_bytes) {
-  if (!need) return MOE_OK;
-  if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
-  if (!aligned16(ws)) return fail(MOE_ERR_UNSUPPORTED, "workspace not 16-byte aligned");
-  if (ws_bytes < need)
-    return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
   return MOE_OK;
 }
 
@@ -119,6 +104,13 @@ moe_status validate_linear(const moe_linear_config* c) {
   return check_dtypes(c->y_dtype, c->dw_dtype);
 }
 
+// Rows of codes are loaded in pieces of 16.
+moe_status check_codes(int32_t in_features) {
+  if (in_features % 16)
+    return fail(MOE_ERR_UNSUPPORTED, "in_features %d not a multiple of 16", in_features);
+  return MOE_OK;
+}
+
 moe_status validate_grouped(const moe_grouped_config* c) {
   if (!c) return fail(MOE_ERR_INVALID_ARG, "config is NULL");
   if (c->num_groups < 1)
@@ -171,6 +163,36 @@ moe::ProductArgs map_args(const MapPlan& m, void* ws) {
   p.K = m.K;
   p.F = m.F;
   p.part = ws ? at<float>(ws, m.part) : nullptr;
+  return p;
+}
+
+// The forward product of codes, in pairs of them, and its workspace (partial sums).
+struct CodesPlan {
+  MapPlan m;
+  bool exact;
+};
+
+void make_codes_plan(int64_t P, int G, int K, int F, int32_t y_dtype, CodesPlan* c) {
+  c->exact = y_dtype == MOE_DTYPE_F32;
+  c->m = MapPlan{};
+  c->m.P = P;
+  c->m.G = G;
+  c->m.K = K / 2;
+  c->m.F = F;
+  c->m.fwd = moe::product_fp8_plan(P, G, K / 2, F, device_cus(), c->exact);
+  const size_t part = moe::product_part_bytes(moe::kForward, P, G, K / 2, F, c->m.fwd);
+  c->m.total = std::max<size_t>(align_up(part), moe::kAlign);
+}
+
+moe::ProductArgs codes_args(const CodesPlan& c, const uint8_t* x, const float* x_scales,
+                            const uint8_t* w, const float* w_scales, void* ws) {
+  moe::ProductArgs p = map_args(c.m, ws);
+  p.a = reinterpret_cast<const uint16_t*>(x);
+  p.b = reinterpret_cast<const uint16_t*>(w);
+  p.a_scale = x_scales;
+  p.b_scale = w_scales;
+  p.a_scale_row = (2 * c.m.K + 127) / 128;
+  p.a_scale_step = 1;
   return p;
 }
 
@@ -352,6 +374,74 @@ moe_status moe_swiglu_backward(const moe_swiglu_config* cfg, const uint16_t* dh,
   MOE_CHECK_LAUNCH(moe::launch_swiglu_grad(dh, gate, up, dgate, dup, h, cfg->rows, cfg->inter, ld,
                                            cfg->limit, stream),
                    "swiglu gradient");
+  return ok();
+}
+
+size_t moe_linear_fp8_workspace_size(const moe_linear_config* cfg) {
+  if (validate_linear(cfg) != MOE_OK || check_codes(cfg->in_features) != MOE_OK) return 0;
+  CodesPlan c;
+  make_codes_plan(cfg->tokens, 1, cfg->in_features, cfg->out_features, cfg->y_dtype, &c);
+  return c.m.total;
+}
+
+moe_status moe_linear_forward_fp8(const moe_linear_config* cfg, const uint8_t* x,
+                                  const float* x_scales, const uint8_t* w, const float* w_scales,
+                                  const float* bias, const uint16_t* residual, void* y,
+                                  uint16_t* z, void* ws, size_t ws_bytes, hipStream_t stream) {
+  moe_status st = validate_linear(cfg);
+  if (st || (st = check_codes(cfg->in_features))) return st;
+  if (!w || !w_scales || (cfg->tokens > 0 && (!x || !x_scales || !y)))
+    return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if ((st = check_pointers({x, x_scales, w, w_scales, bias, residual, y, z}))) return st;
+  CodesPlan c;
+  make_codes_plan(cfg->tokens, 1, cfg->in_features, cfg->out_features, cfg->y_dtype, &c);
+  if ((st = check_workspace(c.m.total, ws, ws_bytes))) return st;
+  if (cfg->tokens == 0) return ok();
+  moe::ProductArgs p = codes_args(c, x, x_scales, w, w_scales, ws);
+  p.bias = bias;
+  p.residual = residual;
+  p.z = z;
+  p.y = y;
+  p.y_f32 = c.exact;
+  p.act = cfg->activation;
+  MOE_CHECK_LAUNCH(moe::launch_product_fp8(p, c.m.fwd, c.exact, stream), "linear fp8 forward");
+  return ok();
+}
+
+size_t moe_grouped_fp8_workspace_size(const moe_grouped_config* cfg) {
+  if (validate_grouped(cfg) != MOE_OK || check_codes(cfg->in_features) != MOE_OK) return 0;
+  CodesPlan c;
+  make_codes_plan(cfg->rows, cfg->num_groups, cfg->in_features, cfg->out_features, cfg->y_dtype,
+                  &c);
+  return c.m.total;
+}
+
+moe_status moe_grouped_forward_fp8(const moe_grouped_config* cfg, const uint8_t* x,
+                                   const float* x_scales, const int32_t* row_ids,
+                                   const int32_t* offsets, const uint8_t* w, const float* w_scales,
+                                   const float* bias, void* y, void* ws, size_t ws_bytes,
+                                   hipStream_t stream) {
+  moe_status st = validate_grouped(cfg);
+  if (st || (st = check_codes(cfg->in_features))) return st;
+  if (!offsets || !w || !w_scales ||
+      (cfg->rows > 0 && ((cfg->x_rows > 0 && (!x || !x_scales)) || !y)))
+    return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if ((st = check_gather(cfg, row_ids))) return st;
+  if ((st = check_pointers({x, x_scales, row_ids, offsets, w, w_scales, bias, y}))) return st;
+  CodesPlan c;
+  make_codes_plan(cfg->rows, cfg->num_groups, cfg->in_features, cfg->out_features, cfg->y_dtype,
+                  &c);
+  if ((st = check_workspace(c.m.total, ws, ws_bytes))) return st;
+  if (cfg->rows == 0) return ok();
+  moe::ProductArgs p = codes_args(c, x, x_scales, w, w_scales, ws);
+  p.offsets = offsets;
+  p.src = row_ids;
+  p.row_div = cfg->row_div;
+  p.x_rows = cfg->x_rows;
+  p.bias = bias;
+  p.y = y;
+  p.y_f32 = c.exact;
+  MOE_CHECK_LAUNCH(moe::launch_product_fp8(p, c.m.fwd, c.exact, stream), "grouped fp8 forward");
   return ok();
 }
 
