@@ -106,6 +106,15 @@ __device__ __forceinline__ F8 load8(const float* p) {
   const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
   return {{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
 }
+// The same with the non-temporal hint, for data that is read once.
+__device__ __forceinline__ F8 read8(const uint16_t* p) {
+  return unpack8(__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
+}
+__device__ __forceinline__ F8 read8(const float* p) {
+  const f32x4 a = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+  const f32x4 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p) + 1);
+  return {{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+}
 // Rounds to nearest even with v_cvt_pk_bf16_f32 (NaN stays NaN).
 __device__ __forceinline__ u32x4 pack8(const F8& f) {
   u32x4 w;

@@ -169,15 +169,12 @@ __device__ __forceinline__ bool find_unit(const ProductArgs& p, int bid, int* sh
 // contractions.  Half and Small: fewer rows or columns, more blocks.  Three,
 // Half and Flat also serve the remainders of groups and the cut tiles in Big's
 // launches.
-// Codes have no Duo (a step is a block of scales, 128 codes), and a Flat of three
-// stages, which leaves their scales room.
-template <int OP, int Q = kNotFp8> using Big = Tile<OP, 256, 256, 2, 4, 2, 3, 64, Q>;
-template <int OP, int Q = kNotFp8> using Half = Tile<OP, 128, 256, 2, 4, 3, 3, 64, Q>;
-template <int OP, int Q = kNotFp8> using Three = Tile<OP, 192, 256, 2, 4, 2, 3, 64, Q>;
+template <int OP> using Big = Tile<OP, 256, 256, 2, 4, 2, 3>;
+template <int OP> using Half = Tile<OP, 128, 256, 2, 4, 3, 3>;
+template <int OP> using Three = Tile<OP, 192, 256, 2, 4, 2, 3>;
 template <int OP> using Duo = Tile<OP, 256, 128, 2, 2, 3, 3, 32>;
-template <int OP, int Q = kNotFp8> using Small = Tile<OP, 64, 64, 2, 2, 4, 4, 64, Q>;
-template <int OP, int Q = kNotFp8>
-using Flat = Tile<OP, 64, 256, 2, 4, Q ? 3 : 4, Q ? 3 : 4, 64, Q>;
+template <int OP> using Small = Tile<OP, 64, 64, 2, 2, 4, 4>;
+template <int OP> using Flat = Tile<OP, 64, 256, 2, 4, 4, 4>;
 
 // Block bid of a product.
 template <int OP, class T, bool GATHER>
@@ -193,22 +190,22 @@ __device__ __forceinline__ void run_block(const ProductArgs& p, int bid, uint8_t
   } else if constexpr (T::BM == 256 && T::BN == 256) {
     // fewer rows, the remainder of a group or a cut tile: the same columns
     // with less of A to load and to multiply
-    static_assert(Flat<OP, T::FP8>::LDS <= T::LDS && Half<OP, T::FP8>::LDS <= T::LDS &&
-                      Three<OP, T::FP8>::LDS <= T::LDS,
+    static_assert(Flat<OP>::RING <= T::RING && Half<OP>::RING <= T::RING &&
+                      Three<OP>::RING <= T::RING,
                   "the same LDS");
-    static_assert(Flat<OP, T::FP8>::THREADS == T::THREADS && Half<OP, T::FP8>::THREADS == T::THREADS &&
-                      Three<OP, T::FP8>::THREADS == T::THREADS,
+    static_assert(Flat<OP>::THREADS == T::THREADS && Half<OP>::THREADS == T::THREADS &&
+                      Three<OP>::THREADS == T::THREADS,
                   "and waves");
     if (un.rows <= 64) {
-      product_tile<OP, Flat<OP, T::FP8>, false, false>(p, smem, un);
+      product_tile<OP, Flat<OP>, false, false>(p, smem, un);
       return;
     }
     if (un.rows <= 128) {
-      product_tile<OP, Half<OP, T::FP8>, false, false>(p, smem, un);
+      product_tile<OP, Half<OP>, false, false>(p, smem, un);
       return;
     }
     if (un.rows <= 192) {
-      product_tile<OP, Three<OP, T::FP8>, false, false>(p, smem, un);
+      product_tile<OP, Three<OP>, false, false>(p, smem, un);
       return;
     }
   }
@@ -217,7 +214,7 @@ __device__ __forceinline__ void run_block(const ProductArgs& p, int bid, uint8_t
 
 template <int OP, class T, bool GATHER>
 __global__ __launch_bounds__(T::THREADS, 2) void product_kernel(ProductArgs p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::RING];
   run_block<OP, T, GATHER>(p, blockIdx.x, smem);
 }
 

@@ -20,10 +20,6 @@
 //    dimension cost no branches and no operand needs padding.
 //  * A and B have rings of SA and SB stages; s_waitcnt vmcnt plus a bare
 //    barrier order them, so later stages stay in flight.
-//  * Codes in 8 bits (FP8 tiles, forward product) travel as rows of half as many
-//    16-bit values: a step is 128 codes, one block of the scales, in the same
-//    128 bytes.  Products of a step are summed on their own and added times the
-//    scales of their row and column block, in fp32.
 //  * The fp32 tile leaves through LDS in whole rows (finish8): bias,
 //    activation and residual act on eight consecutive columns per thread, and
 //    stores are whole lines.
@@ -45,10 +41,6 @@ namespace {
 typedef __attribute__((address_space(3))) void lds_void;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-struct U32x8 {
-  u32x4 lo, hi;
-};
 
 // Buffers are described with kRecords bytes whatever they hold: what keeps a
 // lane inside its operand is its offset, kOutside where it has nothing to read.
@@ -181,22 +173,8 @@ struct Panel {
   }
 };
 
-// How a tile multiplies codes in 8 bits.
-//
-// kNative: v_mfma_f32_32x32x64_f8f6f4, twice the bf16 rate.  It sums the eight
-// products of consecutive codes in fixed point, cut 2^-13 below the largest of
-// them (measured: a product 2^-14 of its neighbour is lost, one of another eight
-// is not), and everything else in fp32: of normal values a block of 128 is off
-// by 1.4e-5 of itself in the 2-norm, little beside the 1.7e-3 of a bf16 result,
-// for which alone it is used.
-// kExact: codes widened to bf16, which holds them, on the bf16 matrix cores:
-// exact products, fp32 sums, for fp32 results.
-enum Fp8Kind : int { kNotFp8 = 0, kNative = 1, kExact = 2 };
-
-template <int OP, int BM_, int BN_, int WM_, int WN_, int SA_, int SB_, int BK_ = 64,
-          int FP8_ = kNotFp8>
+template <int OP, int BM_, int BN_, int WM_, int WN_, int SA_, int SB_, int BK_ = 64>
 struct Tile {
-  static constexpr int FP8 = FP8_;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, SA = SA_, SB = SB_, BK = BK_;
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr int MB = BM / WM / 32, NB = BN / WN / 32;  // 32 x 32 blocks per wave
@@ -205,14 +183,6 @@ struct Tile {
   static constexpr int JA = PA::PIECES / NW, JB = PB::PIECES / NW;  // pieces per wave and stage
   static constexpr int KS = BK / 16;
   static constexpr int RING = SA * PA::BYTES + SB * PB::BYTES;
-  // Codes: the rows' scales of a step.  Equal rings carry them as one more
-  // piece per wave (the waves without rows to fetch load nothing into a place of
-  // their own, so that every wave counts the same loads); split rings leave no
-  // room in LDS, and their waits cover loads into registers a step ahead.
-  static constexpr int JS = FP8 && SA == SB ? 1 : 0;
-  static constexpr int SWAVES = BM / 64;
-  static constexpr int SBYTES = BM * 4;
-  static constexpr int LDS = RING + (JS ? SA * SBYTES + 256 : 0);
   // the fp32 tile leaves in passes that fit the ring
   static constexpr int NEED = (BM * BN * 4 + RING - 1) / RING;
   static constexpr int PASSES = MB % NEED == 0 ? NEED : MB;
@@ -220,493 +190,20 @@ struct Tile {
                     BM * BN * 4 / PASSES <= RING,
                 "tile shape");
   static_assert(SA == SB || (SA == 2 && SB > 2), "ring depths");
-  static_assert((SB - 1) * (JA + JB + JS) < 64, "vmcnt budget");
-  static_assert(!FP8 || (OP == kForward && BK == 64 && BM % 64 == 0 && SWAVES <= NW), "codes");
+  static_assert((SB - 1) * (JA + JB) < 64, "vmcnt budget");
 };
 
-// DB (weight gradient): the tile also sums dy over the rows, by one product
-// more per 16 rows with a matrix of ones; the waves side by side take a block
-// of 32 out features each.
-template <int OP, class T, bool GATHER, bool DB>
-__device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem, const Unit& un) {
-  using PA = typename T::PA;
-  using PB = typename T::PB;
+// The sums of a tile leave: finished by rows (finish8, put_grad8), or as they are
+// into this range's part.  acc[mb][nb]: lane l holds row 32 mb + l % 32 and, for
+// r = 4 g .. 4 g + 3, columns 8 g + 4 (l / 32) + 0..3 of block nb.
+template <int OP, class T>
+__device__ __forceinline__ void tile_leaves(const ProductArgs& p, uint8_t* smem, const Unit& un,
+                                            f32x16 (&acc)[T::MB][T::NB], int wm, int wn) {
   const int N = OP == kForward ? p.F : p.K;
-  const int L = OP == kForward ? p.K : OP == kInputGrad ? p.F : un.len;
-  constexpr int kStep = T::BK;
-  const int KT = (L + kStep - 1) / kStep;
-  const int per = (KT + p.splits - 1) / p.splits;
-  const int k_first = min(KT, un.split * per), k_last = min(KT, k_first + per);
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wid / T::WN, wn = wid % T::WN;
   const int cols = min(T::BN, N - un.col0);
-
-  // ---- sources: per lane a byte offset from a base that moves with the step
-  const char *abase, *bbase;
-  int64_t astep, bstep;
-  if (OP == kWeightGrad) {
-    abase = reinterpret_cast<const char*>(p.a + static_cast<int64_t>(un.begin) * p.F + un.row0);
-    astep = static_cast<int64_t>(kStep) * p.F * 2;
-    if (GATHER) {
-      bbase = reinterpret_cast<const char*>(p.b + un.col0);
-      bstep = 0;
-    } else {
-      bbase = reinterpret_cast<const char*>(p.b + static_cast<int64_t>(un.begin) * p.K + un.col0);
-      bstep = static_cast<int64_t>(kStep) * p.K * 2;
-    }
-  } else {
-    const int64_t wsize = static_cast<int64_t>(p.F) * p.K;
-    const uint16_t* w = p.b + un.g * wsize;
-    astep = kStep * 2;
-    if (OP == kForward && p.src) {
-      abase = reinterpret_cast<const char*>(p.a);
-    } else {
-      abase = reinterpret_cast<const char*>(p.a + static_cast<int64_t>(un.row0) * L);
-    }
-    if (OP == kForward) {
-      bbase = reinterpret_cast<const char*>(w + static_cast<int64_t>(un.col0) * L);
-      bstep = kStep * 2;
-    } else {
-      bbase = reinterpret_cast<const char*>(w + un.col0);
-      bstep = static_cast<int64_t>(kStep) * N * 2;
-    }
-  }
-  uint32_t aoff[T::JA], boff[T::JB];
-  bool atail[T::JA], btail[T::JB];  // the lane's values lie behind L in the last step
-  const int lim = L - (KT - 1) * kStep;
-#pragma unroll
-  for (int j = 0; j < T::JA; ++j) {
-    const int row = PA::RPP * (wid * T::JA + j) + lane / PA::CPR;
-    const int chunk = (lane % PA::CPR) ^ PA::swz(row);
-    atail[j] = (OP == kWeightGrad ? row : chunk * 8) >= lim;
-    if (OP == kWeightGrad) {
-      aoff[j] = chunk * 8 < p.F - un.row0 ? static_cast<uint32_t>(row) * p.F * 2 + chunk * 16
-                                          : kOutside;
-    } else {
-      int64_t s = row;
-      if (row >= un.rows)
-        s = -1;
-      else if (OP == kForward && p.src)
-        s = source_row(p, un.row0 + row);
-      aoff[j] = s >= 0 ? static_cast<uint32_t>(s * L * 2 + chunk * 16) : kOutside;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < T::JB; ++j) {
-    const int row = PB::RPP * (wid * T::JB + j) + lane / PB::CPR;
-    const int chunk = (lane % PB::CPR) ^ PB::swz(row);
-    btail[j] = (OP == kForward ? chunk * 8 : row) >= lim;
-    if (OP == kForward) {
-      boff[j] = row < cols ? static_cast<uint32_t>(row) * L * 2 + chunk * 16 : kOutside;
-    } else {
-      const uint32_t r = GATHER ? 0 : static_cast<uint32_t>(row) * N * 2;
-      // db alone (no y): x is not read
-      boff[j] = chunk * 8 < cols && (OP != kWeightGrad || p.y) ? r + chunk * 16 : kOutside;
-    }
-  }
-  uint8_t* const aring = smem;
-  uint8_t* const bring = smem + T::SA * PA::BYTES;
-  // Codes: one loop for all steps, whose loads of stages behind the last see an
-  // empty buffer.
-  auto records = [&](int kt) MOE_INLINE {
-    return static_cast<int>(!T::FP8 || kt < k_last ? kRecords : 0u);
-  };
-  auto load = [&](const char* base, int64_t step, int kt, uint32_t off, uint8_t* lds) MOE_INLINE {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(base + kt * step), 0, records(kt), 0x00027000);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, 0, 0, 0);
-  };
-  // ---- codes: the scales of this lane's rows, and of the wave's columns
-  [[maybe_unused]] const int KB = KT;  // blocks of a row of codes
-  [[maybe_unused]] const char* sbase = nullptr;
-  [[maybe_unused]] int64_t sstep = 0;
-  [[maybe_unused]] uint32_t soff = kOutside;   // equal rings: the row whose scale this lane fetches
-  [[maybe_unused]] uint32_t srow[T::MB];       // split rings: the rows that it multiplies
-  [[maybe_unused]] const float* wscale = nullptr;
-  if constexpr (T::FP8) {
-    const bool gather = p.src != nullptr && !p.a_scale_ready;
-    sbase = reinterpret_cast<const char*>(p.a_scale);
-    if (!gather) sbase += static_cast<int64_t>(un.row0) * p.a_scale_row * 4;
-    sstep = p.a_scale_step * 4;
-    auto at = [&](int row) MOE_INLINE {
-      if (row >= un.rows) return kOutside;
-      const int64_t s = gather ? source_row(p, un.row0 + row) : row;
-      return s >= 0 ? static_cast<uint32_t>(s * p.a_scale_row * 4) : kOutside;
-    };
-    if (T::JS) {
-      if (wid < T::SWAVES) soff = at(64 * wid + lane);
-    } else {
-#pragma unroll
-      for (int mb = 0; mb < T::MB; ++mb)
-        srow[mb] = at(wm * (T::BM / T::WM) + 32 * mb + (lane & 31));
-    }
-    const int fblocks = (N + 127) / 128;
-    const int fb = min((un.col0 + wn * (T::BN / T::WN)) / 128, fblocks - 1);
-    wscale = p.b_scale + (static_cast<int64_t>(un.g) * fblocks + fb) * KB;
-    static_assert(!T::FP8 || 128 % (T::BN / T::WN) == 0, "a wave's columns share their scale");
-  }
-  [[maybe_unused]] uint8_t* const sring = smem + T::RING;
-  [[maybe_unused]] float ws_held = 0.0f;  // lane i: the column block's scale of step i of 64
-  [[maybe_unused]] float rs_next[T::MB];  // split rings: the rows' scales of the step to come
-  auto fetch_scales = [&](int kt) MOE_INLINE {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(sbase + kt * sstep), 0, records(kt), 0x00027000);
-#pragma unroll
-    for (int mb = 0; mb < T::MB; ++mb)
-      rs_next[mb] = __builtin_bit_cast(
-          float, __builtin_amdgcn_raw_buffer_load_b32(r, srow[mb], 0, 0));
-  };
-  auto issue_s = [&](int kt) MOE_INLINE {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(sbase + kt * sstep), 0, records(kt), 0x00027000);
-    uint8_t* const to = wid < T::SWAVES
-                            ? sring + ((kt - k_first) % T::SA) * T::SBYTES + wid * 256
-                            : sring + T::SA * T::SBYTES;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 4, soff, 0, 0, 0);
-  };
-  auto issue_a = [&](int kt, int j) MOE_INLINE {
-    const uint32_t off = (kt == KT - 1 && atail[j]) ? kOutside : aoff[j];
-    load(abase, astep, kt, off,
-         aring + ((kt - k_first) % T::SA) * PA::BYTES + (wid * T::JA + j) * 1024);
-  };
-  // Gathered rows of the weight gradient: each lane loads the sources of its
-  // rows of a stage one step before the stage is requested and ahead of that
-  // step's other loads, so that the ring's own wait covers them.
-  int ids[T::JB], ids_now[T::JB];
-  auto use_ids = [&]() MOE_INLINE {
-    if constexpr (GATHER)
-#pragma unroll
-      for (int j = 0; j < T::JB; ++j) ids_now[j] = ids[j];
-  };
-  auto fetch_ids = [&](int kt) MOE_INLINE {
-    if constexpr (GATHER) {
-      if (kt < k_last) {
-        const int32_t* s = p.src + un.begin + kt * kStep;  // into the padding at most
-#pragma unroll
-        for (int j = 0; j < T::JB; ++j)
-          ids[j] = s[PB::RPP * (wid * T::JB + j) + lane / PB::CPR];
-      }
-    }
-  };
-  auto issue_b = [&](int kt, int j) MOE_INLINE {
-    uint32_t off = boff[j];
-    if constexpr (GATHER) {
-      const int s = ids_now[j];
-      off = s < 0 || off == kOutside || (kt == KT - 1 && btail[j])
-                ? kOutside
-                : off + static_cast<uint32_t>(s) * p.K * 2;
-    } else {
-      off = (kt == KT - 1 && btail[j]) ? kOutside : off;
-    }
-    load(bbase, bstep, kt, off,
-         bring + ((kt - k_first) % T::SB) * PB::BYTES + (wid * T::JB + j) * 1024);
-  };
-
-  // ---- fragments and products
-  int abase_l[T::MB], bbase_l[T::NB];
-#pragma unroll
-  for (int mb = 0; mb < T::MB; ++mb)
-    abase_l[mb] = PA::frag_base(wm * (T::BM / T::WM) + 32 * mb, lane);
-#pragma unroll
-  for (int nb = 0; nb < T::NB; ++nb)
-    bbase_l[nb] = PB::frag_base(wn * (T::BN / T::WN) + 32 * nb, lane);
-  f32x16 acc[T::MB][T::NB];
-#pragma unroll
-  for (int mb = 0; mb < T::MB; ++mb)
-#pragma unroll
-    for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
-  // db: the wave's blocks of out features are wn, wn + WN, ..
-  constexpr int DBN = (T::MB + T::WN - 1) / T::WN;
-  f32x16 dbacc[DBN];
-  // (read on its own: chosen among the wave's fragments, the compiler would
-  // index them in scratch memory)
-  int dbbase[DBN];
-#pragma unroll
-  for (int i = 0; i < DBN; ++i) {
-    dbacc[i] = f32x16{};
-    dbbase[i] = PA::frag_base(wm * (T::BM / T::WM) + 32 * ((wn + i * T::WN) % T::MB), lane);
-  }
-  const __bf16 one = static_cast<__bf16>(1.0f);
-  const bf16x8 ones{one, one, one, one, one, one, one, one};
-
-  bf16x8 af[2][T::MB], bf[2][T::NB];
-  bf16x8 dbf[2][DBN];
-  auto load_frags = [&](int kt, int ks, int set) MOE_INLINE {
-    uint8_t* sa = aring + ((kt - k_first) % T::SA) * PA::BYTES;
-    uint8_t* sb = bring + ((kt - k_first) % T::SB) * PB::BYTES;
-#pragma unroll
-    for (int nb = 0; nb < T::NB; ++nb) bf[set][nb] = PB::frag(sb, bbase_l[nb], ks, lane);
-#pragma unroll
-    for (int mb = 0; mb < T::MB; ++mb) af[set][mb] = PA::frag(sa, abase_l[mb], ks, lane);
-    if constexpr (DB)
-#pragma unroll
-      for (int i = 0; i < DBN; ++i) dbf[set][i] = PA::frag(sa, dbbase[i], ks, lane);
-  };
-  // The rings.  Step kt multiplies stage kt.  Before its last products, with
-  // all of the stage's fragments in registers, the waves wait for stage kt + 1
-  // and meet at a barrier, so that the first fragments of the next step load
-  // under these products and no step begins with empty registers.  After the
-  // barrier the slots of stage kt are free.  Split rings (SA == 2 < SB): A(kt +
-  // 2) is requested right there, B(kt + SB - 1) between the products before;
-  // loads return in order, so at the barrier only that B stage may be in
-  // flight.  Equal rings: both are requested S - 1 steps ahead between the
-  // products.
-  constexpr bool SPLIT = T::SA != T::SB;
-  constexpr int REFILLS = SPLIT ? T::JB : T::JA + T::JB + T::JS;
-  auto refill = [&](int kt, int d) MOE_INLINE {
-    if (SPLIT)
-      issue_b(kt + T::SB - 1, d);
-    else if (d < T::JA)
-      issue_a(kt + T::SB - 1, d);
-    else if (d < T::JA + T::JB)
-      issue_b(kt + T::SB - 1, d - T::JA);
-    else
-      issue_s(kt + T::SB - 1);
-  };
-  auto meet = [&](int kt) MOE_INLINE {
-    if (T::FP8 || kt + T::SB - 1 < k_last)
-      wait_loads<(SPLIT ? T::JB : (T::SB - 2) * (T::JA + T::JB + T::JS))>();
-    else
-      wait_loads<0>();
-    // the wave's reads of stage kt have returned before another wave refills
-    // its slots
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (SPLIT && (T::FP8 || kt + 2 < k_last))
-#pragma unroll
-      for (int j = 0; j < T::JA; ++j) issue_a(kt + 2, j);
-  };
-  // Codes.  A fragment's 64 codes of a row (native) are the chunks c, c + 1 of
-  // its lane; which codes meet in which product is the same for both operands,
-  // and that is all that a sum over them asks.
-  [[maybe_unused]] auto fp8_steps = [&]() MOE_INLINE {
-    if constexpr (T::FP8) {
-      typedef int i32x8 __attribute__((ext_vector_type(8)));
-      float rs[T::MB];
-      auto use_scales = [&](int kt) MOE_INLINE {  // times the columns' scale
-        const float w = __builtin_bit_cast(
-            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws_held), (kt - k_first) & 63));
-#pragma unroll
-        for (int mb = 0; mb < T::MB; ++mb) {
-          if (T::JS)
-            rs_next[mb] = *reinterpret_cast<const float*>(
-                sring + ((kt - k_first) % T::SA) * T::SBYTES +
-                (wm * (T::BM / T::WM) + 32 * mb + (lane & 31)) * 4);
-          rs[mb] = rs_next[mb] * w;
-        }
-      };
-      // A half of a step: two chunks of a row, 32 codes of each lane's half.
-      u32x4 bq[T::NB][4], aq[4];
-      auto load_b = [&](int kt, int half) MOE_INLINE {
-        uint8_t* sb = bring + ((kt - k_first) % T::SB) * PB::BYTES;
-#pragma unroll
-        for (int nb = 0; nb < T::NB; ++nb)
-#pragma unroll
-          for (int c = 2 * half; c < 2 * half + 2; ++c)
-            bq[nb][c] = __builtin_bit_cast(u32x4, PB::frag(sb, bbase_l[nb], c, lane));
-      };
-      auto load_a = [&](int kt, int mb, int half) MOE_INLINE {
-        uint8_t* sa = aring + ((kt - k_first) % T::SA) * PA::BYTES;
-#pragma unroll
-        for (int c = 2 * half; c < 2 * half + 2; ++c)
-          aq[c] = __builtin_bit_cast(u32x4, PA::frag(sa, abase_l[mb], c, lane));
-      };
-      // Block nb's sums of the step in the wave's present row block.
-      f32x16 t[T::NB];
-      auto multiply = [&](int nb, int half) MOE_INLINE {
-        const u32x4 b0 = bq[nb][2 * half], b1 = bq[nb][2 * half + 1];
-        const u32x4 a0 = aq[2 * half], a1 = aq[2 * half + 1];
-        f32x16 v = half ? t[nb] : f32x16{};
-        if constexpr (T::FP8 == kNative) {
-          const i32x8 b = __builtin_bit_cast(i32x8, U32x8{b0, b1});
-          const i32x8 a = __builtin_bit_cast(i32x8, U32x8{a0, a1});
-          v = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, v, 0, 0, 0, 0, 0, 0);
-        } else {
-          v = mfma32(e4m3x8_to_bf16(b0[0], b0[1]), e4m3x8_to_bf16(a0[0], a0[1]), v);
-          v = mfma32(e4m3x8_to_bf16(b0[2], b0[3]), e4m3x8_to_bf16(a0[2], a0[3]), v);
-          v = mfma32(e4m3x8_to_bf16(b1[0], b1[1]), e4m3x8_to_bf16(a1[0], a1[1]), v);
-          v = mfma32(e4m3x8_to_bf16(b1[2], b1[3]), e4m3x8_to_bf16(a1[2], a1[3]), v);
-        }
-        t[nb] = v;
-      };
-      auto add = [&](int mb, int nb, float scale) MOE_INLINE {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[mb][nb][i] = fmaf(scale, t[nb][i], acc[mb][nb][i]);
-      };
-      // A row block's sums are added when the next one's products replace them
-      // one by one, so that the additions run under products; the last block's
-      // in the next step, with the scale of its own (`last`; at first 0, times
-      // sums of 0).  Fragments are replaced as soon as their products are issued.
-      float last = 0.0f;
-#pragma unroll
-      for (int nb = 0; nb < T::NB; ++nb) t[nb] = f32x16{};
-      auto step = [&](int kt) MOE_INLINE {
-        constexpr int FIRST = T::MB - 1;  // row blocks before the barrier
-        constexpr int PER = FIRST > 0 ? (REFILLS + FIRST - 1) / FIRST : REFILLS;
-        use_scales(kt);
-        if (((kt + 1 - k_first) & 63) == 0) {
-          ws_held = wscale[min(kt + 1 + lane, KB - 1)];
-          wait_loads<0>();  // (here, so that no other step waits for it)
-        }
-        if (!T::JS) fetch_scales(kt + 1);
-#pragma unroll
-        for (int mb = 0; mb < T::MB; ++mb) {
-          const bool final = mb + 1 == T::MB;
-          if (final) {
-#pragma unroll
-            for (int d = FIRST * PER; d < REFILLS; ++d) refill(kt, d);
-            meet(kt);
-          }
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int nb = 0; nb < T::NB; ++nb) {
-              if (half == 0) add(mb ? mb - 1 : T::MB - 1, nb, mb ? rs[mb - 1] : last);
-              __builtin_amdgcn_sched_barrier(0);  // (the products take the sums' registers)
-              multiply(nb, half);
-              __builtin_amdgcn_sched_barrier(0);
-            }
-            if (!final) {
-              load_a(kt, mb + 1, half);
-            } else {
-              load_a(kt + 1, 0, half);
-              load_b(kt + 1, half);
-            }
-          }
-          if (!final)
-#pragma unroll
-            for (int d = mb * PER; d < (mb + 1) * PER && d < REFILLS; ++d) refill(kt, d);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        last = rs[T::MB - 1];
-      };
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        load_b(k_first, half);
-        load_a(k_first, 0, half);
-      }
-      // (a first step of its own, which the compiler would make, spills registers)
-#pragma clang loop unroll(disable)
-      for (int kt = k_first; kt < k_last; ++kt) step(kt);
-#pragma unroll
-      for (int nb = 0; nb < T::NB; ++nb) add(T::MB - 1, nb, last);
-    }
-  };
-  if (k_first < k_last) {
-    if constexpr (T::FP8) {  // ahead of the rings' loads, whose first wait covers these
-      ws_held = wscale[min(k_first + lane, KB - 1)];
-      if (!T::JS) fetch_scales(k_first);
-    }
-#pragma unroll
-    for (int s = 0; s < T::SB - 1; ++s)
-      if (T::FP8 || k_first + s < k_last) {
-        fetch_ids(k_first + s);
-        use_ids();
-        if (s < T::SA - 1)
-#pragma unroll
-          for (int j = 0; j < T::JA; ++j) issue_a(k_first + s, j);
-#pragma unroll
-        for (int j = 0; j < T::JB; ++j) issue_b(k_first + s, j);
-        if (T::JS) issue_s(k_first + s);
-      }
-    fetch_ids(k_first + T::SB - 1);  // for the first step's refill
-    if (T::FP8 || k_first + T::SB - 2 < k_last)
-      wait_loads<(T::SB - 2) * (SPLIT ? T::JB : T::JA + T::JB + T::JS)>();
-    else
-      wait_loads<0>();
-    asm volatile("s_barrier" ::: "memory");
-    if (SPLIT && (T::FP8 || k_first + 1 < k_last))
-#pragma unroll
-      for (int j = 0; j < T::JA; ++j) issue_a(k_first + 1, j);
-    constexpr int EARLY = (T::KS - 1) * T::MB * T::NB;  // products before the barrier
-    constexpr int EVERY = EARLY / REFILLS > 0 ? EARLY / REFILLS : 1;
-    const bool has_work = wm * (T::BM / T::WM) < un.rows && wn * (T::BN / T::WN) < cols;
-    if (!has_work && !DB) {
-      for (int kt = k_first; kt < k_last; ++kt) {
-        use_ids();
-        fetch_ids(kt + T::SB);
-        if (T::FP8 || kt + T::SB - 1 < k_last)
-#pragma unroll
-          for (int d = 0; d < REFILLS; ++d) refill(kt, d);
-        if (T::FP8 || kt + 1 < k_last) meet(kt);
-      }
-    } else if constexpr (T::FP8) {
-      fp8_steps();
-    } else {
-      load_frags(k_first, 0, 0);
-      auto step = [&](int kt, auto REFILL) MOE_INLINE {
-        constexpr bool more = decltype(REFILL)::value;
-        if (more) {
-          use_ids();
-          fetch_ids(kt + T::SB);
-        }
-#pragma unroll
-        for (int ks = 0; ks < T::KS; ++ks) {
-          if (ks + 1 < T::KS) {
-            load_frags(kt, ks + 1, (ks + 1) & 1);
-          } else {
-            if (more && EARLY / EVERY < REFILLS)
-#pragma unroll
-              for (int d = EARLY / EVERY; d < REFILLS; ++d) refill(kt, d);
-            if (kt + 1 < k_last) {
-              meet(kt);
-              load_frags(kt + 1, 0, 0);
-            }
-          }
-          if constexpr (DB)
-#pragma unroll
-            for (int i = 0; i < DBN; ++i) dbacc[i] = mfma32(ones, dbf[ks & 1][i], dbacc[i]);
-#pragma unroll
-          for (int mb = 0; mb < T::MB; ++mb)
-#pragma unroll
-            for (int nb = 0; nb < T::NB; ++nb) {
-              acc[mb][nb] = mfma32(bf[ks & 1][nb], af[ks & 1][mb], acc[mb][nb]);
-              const int i = (ks * T::MB + mb) * T::NB + nb;
-              if (more && i < EARLY && i % EVERY == EVERY - 1 && i / EVERY < REFILLS)
-                refill(kt, i / EVERY);
-            }
-          if constexpr (T::MB * T::NB == 8 && T::NW == 8) {
-            // Big: three fragment reads, then one after every two products
-            // (+1 to 1.5% on 8192 cubed; one after each product, or half of
-            // them first: +-0; the smaller tiles lose 2% to any such order).
-            __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-              __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
-              __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            }
-            __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      };
-      static_assert(T::KS % 2 == 0, "the next step's first fragments take set 0");
-      int kt = k_first;
-      for (; kt + T::SB - 1 < k_last; ++kt) step(kt, std::true_type{});
-      for (; kt < k_last; ++kt) step(kt, std::false_type{});
-    }
-  }
-
-  if constexpr (T::FP8) wait_loads<0>();  // (of stages behind the last, whose zeros go to LDS)
-
-  // ---- the tile leaves.  acc[mb][nb]: lane l holds row 32 mb + l % 32 and,
-  // for r = 4 g .. 4 g + 3, columns 8 g + 4 (l / 32) + 0..3 of block nb.
+  const int tid = threadIdx.x, lane = tid & 63;
   const int64_t out_row0 = (OP == kWeightGrad ? static_cast<int64_t>(un.g) * p.F : 0) + un.row0;
   const int64_t out_rows = OP == kWeightGrad ? static_cast<int64_t>(p.G) * p.F : p.P;
-  if constexpr (DB) {
-#pragma unroll
-    for (int i = 0; i < DBN; ++i) {
-      const int b = wn + i * T::WN, r = wm * (T::BM / T::WM) + 32 * b + (lane & 31);
-      if (b < T::MB && lane < 32 && r < un.rows) {
-        const int64_t at = out_row0 + r;
-        if (p.splits > 1)
-          p.part_db[un.split * out_rows + at] = dbacc[i][0];
-        else
-          p.db[at] = p.accumulate ? p.db[at] + dbacc[i][0] : dbacc[i][0];
-      }
-    }
-  }
-  if (OP == kWeightGrad && !p.y) return;
   // In passes through LDS: the fp32 blocks laid down by rows (16-byte chunks
   // XOR-rotated by the row), then each thread takes eight columns, the same in
   // every row it takes, of rows RSTEP apart: its bias is loaded once, and
@@ -815,6 +312,311 @@ __device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem
   run_pass(std::integral_constant<int, 0>{});
   if constexpr (T::PASSES > 1) run_pass(std::integral_constant<int, 1>{});
   if constexpr (T::PASSES > 2) run_pass(std::integral_constant<int, 2>{});
+}
+
+// DB (weight gradient): the tile also sums dy over the rows, by one product
+// more per 16 rows with a matrix of ones; the waves side by side take a block
+// of 32 out features each.
+template <int OP, class T, bool GATHER, bool DB>
+__device__ __forceinline__ void product_tile(const ProductArgs& p, uint8_t* smem, const Unit& un) {
+  using PA = typename T::PA;
+  using PB = typename T::PB;
+  const int N = OP == kForward ? p.F : p.K;
+  const int L = OP == kForward ? p.K : OP == kInputGrad ? p.F : un.len;
+  constexpr int kStep = T::BK;
+  const int KT = (L + kStep - 1) / kStep;
+  const int per = (KT + p.splits - 1) / p.splits;
+  const int k_first = min(KT, un.split * per), k_last = min(KT, k_first + per);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wid / T::WN, wn = wid % T::WN;
+  const int cols = min(T::BN, N - un.col0);
+
+  // ---- sources: per lane a byte offset from a base that moves with the step
+  const char *abase, *bbase;
+  int64_t astep, bstep;
+  if (OP == kWeightGrad) {
+    abase = reinterpret_cast<const char*>(p.a + static_cast<int64_t>(un.begin) * p.F + un.row0);
+    astep = static_cast<int64_t>(kStep) * p.F * 2;
+    if (GATHER) {
+      bbase = reinterpret_cast<const char*>(p.b + un.col0);
+      bstep = 0;
+    } else {
+      bbase = reinterpret_cast<const char*>(p.b + static_cast<int64_t>(un.begin) * p.K + un.col0);
+      bstep = static_cast<int64_t>(kStep) * p.K * 2;
+    }
+  } else {
+    const int64_t wsize = static_cast<int64_t>(p.F) * p.K;
+    const uint16_t* w = p.b + un.g * wsize;
+    astep = kStep * 2;
+    if (OP == kForward && p.src) {
+      abase = reinterpret_cast<const char*>(p.a);
+    } else {
+      abase = reinterpret_cast<const char*>(p.a + static_cast<int64_t>(un.row0) * L);
+    }
+    if (OP == kForward) {
+      bbase = reinterpret_cast<const char*>(w + static_cast<int64_t>(un.col0) * L);
+      bstep = kStep * 2;
+    } else {
+      bbase = reinterpret_cast<const char*>(w + un.col0);
+      bstep = static_cast<int64_t>(kStep) * N * 2;
+    }
+  }
+  uint32_t aoff[T::JA], boff[T::JB];
+  bool atail[T::JA], btail[T::JB];  // the lane's values lie behind L in the last step
+  const int lim = L - (KT - 1) * kStep;
+#pragma unroll
+  for (int j = 0; j < T::JA; ++j) {
+    const int row = PA::RPP * (wid * T::JA + j) + lane / PA::CPR;
+    const int chunk = (lane % PA::CPR) ^ PA::swz(row);
+    atail[j] = (OP == kWeightGrad ? row : chunk * 8) >= lim;
+    if (OP == kWeightGrad) {
+      aoff[j] = chunk * 8 < p.F - un.row0 ? static_cast<uint32_t>(row) * p.F * 2 + chunk * 16
+                                          : kOutside;
+    } else {
+      int64_t s = row;
+      if (row >= un.rows)
+        s = -1;
+      else if (OP == kForward && p.src)
+        s = source_row(p, un.row0 + row);
+      aoff[j] = s >= 0 ? static_cast<uint32_t>(s * L * 2 + chunk * 16) : kOutside;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < T::JB; ++j) {
+    const int row = PB::RPP * (wid * T::JB + j) + lane / PB::CPR;
+    const int chunk = (lane % PB::CPR) ^ PB::swz(row);
+    btail[j] = (OP == kForward ? chunk * 8 : row) >= lim;
+    if (OP == kForward) {
+      boff[j] = row < cols ? static_cast<uint32_t>(row) * L * 2 + chunk * 16 : kOutside;
+    } else {
+      const uint32_t r = GATHER ? 0 : static_cast<uint32_t>(row) * N * 2;
+      // db alone (no y): x is not read
+      boff[j] = chunk * 8 < cols && (OP != kWeightGrad || p.y) ? r + chunk * 16 : kOutside;
+    }
+  }
+  uint8_t* const aring = smem;
+  uint8_t* const bring = smem + T::SA * PA::BYTES;
+  auto load = [&](const char* base, int64_t step, int kt, uint32_t off, uint8_t* lds) MOE_INLINE {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(base + kt * step), 0, static_cast<int>(kRecords), 0x00027000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, 0, 0, 0);
+  };
+  auto issue_a = [&](int kt, int j) MOE_INLINE {
+    const uint32_t off = (kt == KT - 1 && atail[j]) ? kOutside : aoff[j];
+    load(abase, astep, kt, off,
+         aring + ((kt - k_first) % T::SA) * PA::BYTES + (wid * T::JA + j) * 1024);
+  };
+  // Gathered rows of the weight gradient: each lane loads the sources of its
+  // rows of a stage one step before the stage is requested and ahead of that
+  // step's other loads, so that the ring's own wait covers them.
+  int ids[T::JB], ids_now[T::JB];
+  auto use_ids = [&]() MOE_INLINE {
+    if constexpr (GATHER)
+#pragma unroll
+      for (int j = 0; j < T::JB; ++j) ids_now[j] = ids[j];
+  };
+  auto fetch_ids = [&](int kt) MOE_INLINE {
+    if constexpr (GATHER) {
+      if (kt < k_last) {
+        const int32_t* s = p.src + un.begin + kt * kStep;  // into the padding at most
+#pragma unroll
+        for (int j = 0; j < T::JB; ++j)
+          ids[j] = s[PB::RPP * (wid * T::JB + j) + lane / PB::CPR];
+      }
+    }
+  };
+  auto issue_b = [&](int kt, int j) MOE_INLINE {
+    uint32_t off = boff[j];
+    if constexpr (GATHER) {
+      const int s = ids_now[j];
+      off = s < 0 || off == kOutside || (kt == KT - 1 && btail[j])
+                ? kOutside
+                : off + static_cast<uint32_t>(s) * p.K * 2;
+    } else {
+      off = (kt == KT - 1 && btail[j]) ? kOutside : off;
+    }
+    load(bbase, bstep, kt, off,
+         bring + ((kt - k_first) % T::SB) * PB::BYTES + (wid * T::JB + j) * 1024);
+  };
+
+  // ---- fragments and products
+  int abase_l[T::MB], bbase_l[T::NB];
+#pragma unroll
+  for (int mb = 0; mb < T::MB; ++mb)
+    abase_l[mb] = PA::frag_base(wm * (T::BM / T::WM) + 32 * mb, lane);
+#pragma unroll
+  for (int nb = 0; nb < T::NB; ++nb)
+    bbase_l[nb] = PB::frag_base(wn * (T::BN / T::WN) + 32 * nb, lane);
+  f32x16 acc[T::MB][T::NB];
+#pragma unroll
+  for (int mb = 0; mb < T::MB; ++mb)
+#pragma unroll
+    for (int nb = 0; nb < T::NB; ++nb) acc[mb][nb] = f32x16{};
+  // db: the wave's blocks of out features are wn, wn + WN, ..
+  constexpr int DBN = (T::MB + T::WN - 1) / T::WN;
+  f32x16 dbacc[DBN];
+  // (read on its own: chosen among the wave's fragments, the compiler would
+  // index them in scratch memory)
+  int dbbase[DBN];
+#pragma unroll
+  for (int i = 0; i < DBN; ++i) {
+    dbacc[i] = f32x16{};
+    dbbase[i] = PA::frag_base(wm * (T::BM / T::WM) + 32 * ((wn + i * T::WN) % T::MB), lane);
+  }
+  const __bf16 one = static_cast<__bf16>(1.0f);
+  const bf16x8 ones{one, one, one, one, one, one, one, one};
+
+  bf16x8 af[2][T::MB], bf[2][T::NB];
+  bf16x8 dbf[2][DBN];
+  auto load_frags = [&](int kt, int ks, int set) MOE_INLINE {
+    uint8_t* sa = aring + ((kt - k_first) % T::SA) * PA::BYTES;
+    uint8_t* sb = bring + ((kt - k_first) % T::SB) * PB::BYTES;
+#pragma unroll
+    for (int nb = 0; nb < T::NB; ++nb) bf[set][nb] = PB::frag(sb, bbase_l[nb], ks, lane);
+#pragma unroll
+    for (int mb = 0; mb < T::MB; ++mb) af[set][mb] = PA::frag(sa, abase_l[mb], ks, lane);
+    if constexpr (DB)
+#pragma unroll
+      for (int i = 0; i < DBN; ++i) dbf[set][i] = PA::frag(sa, dbbase[i], ks, lane);
+  };
+  // The rings.  Step kt multiplies stage kt.  Before its last products, with
+  // all of the stage's fragments in registers, the waves wait for stage kt + 1
+  // and meet at a barrier, so that the first fragments of the next step load
+  // under these products and no step begins with empty registers.  After the
+  // barrier the slots of stage kt are free.  Split rings (SA == 2 < SB): A(kt +
+  // 2) is requested right there, B(kt + SB - 1) between the products before;
+  // loads return in order, so at the barrier only that B stage may be in
+  // flight.  Equal rings: both are requested S - 1 steps ahead between the
+  // products.
+  constexpr bool SPLIT = T::SA != T::SB;
+  constexpr int REFILLS = SPLIT ? T::JB : T::JA + T::JB;
+  auto refill = [&](int kt, int d) MOE_INLINE {
+    if (SPLIT)
+      issue_b(kt + T::SB - 1, d);
+    else if (d < T::JA)
+      issue_a(kt + T::SB - 1, d);
+    else
+      issue_b(kt + T::SB - 1, d - T::JA);
+  };
+  auto meet = [&](int kt) MOE_INLINE {
+    if (kt + T::SB - 1 < k_last)
+      wait_loads<(SPLIT ? T::JB : (T::SB - 2) * (T::JA + T::JB))>();
+    else
+      wait_loads<0>();
+    // the wave's reads of stage kt have returned before another wave refills
+    // its slots
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (SPLIT && kt + 2 < k_last)
+#pragma unroll
+      for (int j = 0; j < T::JA; ++j) issue_a(kt + 2, j);
+  };
+  if (k_first < k_last) {
+#pragma unroll
+    for (int s = 0; s < T::SB - 1; ++s)
+      if (k_first + s < k_last) {
+        fetch_ids(k_first + s);
+        use_ids();
+        if (s < T::SA - 1)
+#pragma unroll
+          for (int j = 0; j < T::JA; ++j) issue_a(k_first + s, j);
+#pragma unroll
+        for (int j = 0; j < T::JB; ++j) issue_b(k_first + s, j);
+      }
+    fetch_ids(k_first + T::SB - 1);  // for the first step's refill
+    if (k_first + T::SB - 2 < k_last)
+      wait_loads<(T::SB - 2) * (SPLIT ? T::JB : T::JA + T::JB)>();
+    else
+      wait_loads<0>();
+    asm volatile("s_barrier" ::: "memory");
+    if (SPLIT && k_first + 1 < k_last)
+#pragma unroll
+      for (int j = 0; j < T::JA; ++j) issue_a(k_first + 1, j);
+    constexpr int EARLY = (T::KS - 1) * T::MB * T::NB;  // products before the barrier
+    constexpr int EVERY = EARLY / REFILLS > 0 ? EARLY / REFILLS : 1;
+    const bool has_work = wm * (T::BM / T::WM) < un.rows && wn * (T::BN / T::WN) < cols;
+    if (!has_work && !DB) {
+      for (int kt = k_first; kt < k_last; ++kt) {
+        use_ids();
+        fetch_ids(kt + T::SB);
+        if (kt + T::SB - 1 < k_last)
+#pragma unroll
+          for (int d = 0; d < REFILLS; ++d) refill(kt, d);
+        if (kt + 1 < k_last) meet(kt);
+      }
+    } else {
+      load_frags(k_first, 0, 0);
+      auto step = [&](int kt, auto REFILL) MOE_INLINE {
+        constexpr bool more = decltype(REFILL)::value;
+        if (more) {
+          use_ids();
+          fetch_ids(kt + T::SB);
+        }
+#pragma unroll
+        for (int ks = 0; ks < T::KS; ++ks) {
+          if (ks + 1 < T::KS) {
+            load_frags(kt, ks + 1, (ks + 1) & 1);
+          } else {
+            if (more && EARLY / EVERY < REFILLS)
+#pragma unroll
+              for (int d = EARLY / EVERY; d < REFILLS; ++d) refill(kt, d);
+            if (kt + 1 < k_last) {
+              meet(kt);
+              load_frags(kt + 1, 0, 0);
+            }
+          }
+          if constexpr (DB)
+#pragma unroll
+            for (int i = 0; i < DBN; ++i) dbacc[i] = mfma32(ones, dbf[ks & 1][i], dbacc[i]);
+#pragma unroll
+          for (int mb = 0; mb < T::MB; ++mb)
+#pragma unroll
+            for (int nb = 0; nb < T::NB; ++nb) {
+              acc[mb][nb] = mfma32(bf[ks & 1][nb], af[ks & 1][mb], acc[mb][nb]);
+              const int i = (ks * T::MB + mb) * T::NB + nb;
+              if (more && i < EARLY && i % EVERY == EVERY - 1 && i / EVERY < REFILLS)
+                refill(kt, i / EVERY);
+            }
+          if constexpr (T::MB * T::NB == 8 && T::NW == 8) {
+            // Big: three fragment reads, then one after every two products
+            // (+1 to 1.5% on 8192 cubed; one after each product, or half of
+            // them first: +-0; the smaller tiles lose 2% to any such order).
+            __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+              __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+              __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      static_assert(T::KS % 2 == 0, "the next step's first fragments take set 0");
+      int kt = k_first;
+      for (; kt + T::SB - 1 < k_last; ++kt) step(kt, std::true_type{});
+      for (; kt < k_last; ++kt) step(kt, std::false_type{});
+    }
+  }
+
+  // ---- the tile leaves
+  const int64_t out_row0 = (OP == kWeightGrad ? static_cast<int64_t>(un.g) * p.F : 0) + un.row0;
+  const int64_t out_rows = OP == kWeightGrad ? static_cast<int64_t>(p.G) * p.F : p.P;
+  if constexpr (DB) {
+#pragma unroll
+    for (int i = 0; i < DBN; ++i) {
+      const int b = wn + i * T::WN, r = wm * (T::BM / T::WM) + 32 * b + (lane & 31);
+      if (b < T::MB && lane < 32 && r < un.rows) {
+        const int64_t at = out_row0 + r;
+        if (p.splits > 1)
+          p.part_db[un.split * out_rows + at] = dbacc[i][0];
+        else
+          p.db[at] = p.accumulate ? p.db[at] + dbacc[i][0] : dbacc[i][0];
+      }
+    }
+  }
+  if (OP == kWeightGrad && !p.y) return;
+  tile_leaves<OP, T>(p, smem, un, acc, wm, wn);
 }
 
 }  // namespace

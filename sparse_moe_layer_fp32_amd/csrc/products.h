@@ -70,6 +70,13 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus);
 bool pair_plan(int64_t P, int G, int K, int F, int cus, ProductPlan* x, ProductPlan* w);
 // The forward product of codes, with K in pairs of them; exact: fp32 results.
 ProductPlan product_fp8_plan(int64_t P, int G, int K, int F, int cus, bool exact);
+// Whether that plan wants the scales of x by steps: by_step[s scale_pitch(P) + r] is
+// row r's (of y) of step s, 0 where x has no such row.
+bool wants_scales_by_step(const ProductPlan& plan);
+inline int64_t scale_pitch(int64_t P) { return (P + 63) / 64 * 64; }
+hipError_t launch_scales_by_step(const float* scales, const int32_t* row_ids, int row_div,
+                                 int64_t x_rows, int64_t P, int steps, float* by_step,
+                                 hipStream_t stream);
 hipError_t launch_product_fp8(const ProductArgs& p, const ProductPlan& plan, bool exact,
                               hipStream_t stream);
 // Bytes of `part` (with part_db behind it) for that plan; 0 when splits == 1.

@@ -166,10 +166,12 @@ moe::ProductArgs map_args(const MapPlan& m, void* ws) {
   return p;
 }
 
-// The forward product of codes, in pairs of them, and its workspace (partial sums).
+// The forward product of codes, in pairs of them, and its workspace: the scales
+// of x by steps, where the tiles want them so, then partial sums.
 struct CodesPlan {
   MapPlan m;
-  bool exact;
+  bool exact, by_step;
+  int steps;
 };
 
 void make_codes_plan(int64_t P, int G, int K, int F, int32_t y_dtype, CodesPlan* c) {
@@ -181,7 +183,10 @@ void make_codes_plan(int64_t P, int G, int K, int F, int32_t y_dtype, CodesPlan*
   c->m.F = F;
   c->m.fwd = moe::product_fp8_plan(P, G, K / 2, F, device_cus(), c->exact);
   const size_t part = moe::product_part_bytes(moe::kForward, P, G, K / 2, F, c->m.fwd);
-  c->m.total = std::max<size_t>(align_up(part), moe::kAlign);
+  c->steps = (K + 127) / 128;
+  c->by_step = moe::wants_scales_by_step(c->m.fwd);
+  c->m.part = c->by_step ? align_up(static_cast<size_t>(moe::scale_pitch(P)) * c->steps * 4) : 0;
+  c->m.total = std::max<size_t>(c->m.part + align_up(part), moe::kAlign);
 }
 
 moe::ProductArgs codes_args(const CodesPlan& c, const uint8_t* x, const float* x_scales,
@@ -191,9 +196,23 @@ moe::ProductArgs codes_args(const CodesPlan& c, const uint8_t* x, const float* x
   p.b = reinterpret_cast<const uint16_t*>(w);
   p.a_scale = x_scales;
   p.b_scale = w_scales;
-  p.a_scale_row = (2 * c.m.K + 127) / 128;
+  p.a_scale_row = c.steps;
   p.a_scale_step = 1;
   return p;
+}
+
+hipError_t forward_codes(const CodesPlan& c, moe::ProductArgs p, void* ws, hipStream_t stream) {
+  if (c.by_step) {
+    float* by_step = at<float>(ws, 0);
+    const hipError_t e = moe::launch_scales_by_step(p.a_scale, p.src, p.row_div, p.x_rows, p.P,
+                                                    c.steps, by_step, stream);
+    if (e != hipSuccess) return e;
+    p.a_scale = by_step;
+    p.a_scale_row = 1;
+    p.a_scale_step = moe::scale_pitch(p.P);
+    p.a_scale_ready = 1;
+  }
+  return moe::launch_product_fp8(p, c.m.fwd, c.exact, stream);
 }
 
 // The input and weight gradients that are wanted of p (with a = dy).
@@ -404,7 +423,7 @@ moe_status moe_linear_forward_fp8(const moe_linear_config* cfg, const uint8_t* x
   p.y = y;
   p.y_f32 = c.exact;
   p.act = cfg->activation;
-  MOE_CHECK_LAUNCH(moe::launch_product_fp8(p, c.m.fwd, c.exact, stream), "linear fp8 forward");
+  MOE_CHECK_LAUNCH(forward_codes(c, p, ws, stream), "linear fp8 forward");
   return ok();
 }
 
@@ -441,7 +460,7 @@ moe_status moe_grouped_forward_fp8(const moe_grouped_config* cfg, const uint8_t*
   p.bias = bias;
   p.y = y;
   p.y_f32 = c.exact;
-  MOE_CHECK_LAUNCH(moe::launch_product_fp8(p, c.m.fwd, c.exact, stream), "grouped fp8 forward");
+  MOE_CHECK_LAUNCH(forward_codes(c, p, ws, stream), "grouped fp8 forward");
   return ok();
 }
 

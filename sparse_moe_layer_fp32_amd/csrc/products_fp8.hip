@@ -5,8 +5,9 @@
 //
 // on the tiles of the bf16 products (product_tile.h), whose steps of 128 bytes
 // are one block of codes each.  For bf16 results the tiles multiply codes as they
-// are, for fp32 results codes widened to bf16 (Fp8Kind says why).
+// are, for fp32 results codes widened to bf16 (codes_tile.h).
 
+#include "codes_tile.h"
 #include "product_blocks.h"
 
 namespace moe {
@@ -86,6 +87,32 @@ __global__ __launch_bounds__(64 * kThinWaves) void product_thin_fp8(ProductArgs 
              un.col0 + c, p.F);
 }
 
+// A block takes 64 rows and 32 steps through LDS, reading rows and writing steps.
+constexpr int kTurnRows = 64, kTurnSteps = 32;
+
+__global__ __launch_bounds__(256) void scales_by_step_kernel(
+    const float* __restrict__ scales, const int32_t* __restrict__ row_ids, int row_div,
+    int64_t x_rows, int64_t P, int steps, int64_t pitch, float* __restrict__ by_step) {
+  __shared__ float tile[kTurnSteps][kTurnRows + 1];
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kTurnRows;
+  const int s0 = blockIdx.y * kTurnSteps;
+  const int s = threadIdx.x % kTurnSteps;
+#pragma unroll
+  for (int i = threadIdx.x / kTurnSteps; i < kTurnRows; i += 256 / kTurnSteps) {
+    int64_t src = r0 + i < P ? r0 + i : -1;
+    if (src >= 0 && row_ids) {
+      const int id = row_ids[src];
+      src = id >= 0 && id / row_div < x_rows ? id / row_div : -1;
+    }
+    tile[s][i] = src >= 0 && s0 + s < steps ? scales[src * steps + s0 + s] : 0.0f;
+  }
+  __syncthreads();
+  const int r = threadIdx.x % kTurnRows;
+#pragma unroll
+  for (int i = threadIdx.x / kTurnRows; i < kTurnSteps; i += 256 / kTurnRows)
+    if (s0 + i < steps) by_step[(s0 + i) * pitch + r0 + r] = tile[i][r];
+}
+
 template <int COLS>
 hipError_t launch_thin_fp8(const ProductArgs& p, hipStream_t stream) {
   const int64_t units =
@@ -95,18 +122,62 @@ hipError_t launch_thin_fp8(const ProductArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <class T>
+__global__ __launch_bounds__(T::THREADS, 2) void codes_kernel(ProductArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+  Unit un;
+  if (!find_unit<kForward, T::BM, T::BN, T::THREADS>(p, blockIdx.x, reinterpret_cast<int*>(smem),
+                                                     &un))
+    return;
+  if constexpr (T::BM == 256) {
+    // fewer rows, the remainder of a group or a cut tile: the same columns with
+    // less of x to load and to multiply
+    using Three = CodesThree<T::KIND>;
+    using Half = CodesHalf<T::KIND>;
+    using Flat = CodesFlat<T::KIND>;
+    static_assert(Flat::LDS <= T::LDS && Half::LDS <= T::LDS && Three::LDS <= T::LDS &&
+                      Flat::THREADS == T::THREADS && Half::THREADS == T::THREADS &&
+                      Three::THREADS == T::THREADS,
+                  "the same LDS and waves");
+    if (un.rows <= 64) return codes_tile<Flat>(p, smem, un);
+    if (un.rows <= 128) return codes_tile<Half>(p, smem, un);
+    if (un.rows <= 192) return codes_tile<Three>(p, smem, un);
+  }
+  codes_tile<T>(p, smem, un);
+}
+
+template <class T>
+hipError_t launch_codes(ProductArgs p, hipStream_t stream) {
+  const unsigned grid = grid_of<kForward, T>(&p);
+  if (grid == 0) return hipSuccess;
+  codes_kernel<T><<<grid, T::THREADS, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
 template <int Q>
 hipError_t launch_shape(const ProductArgs& p, int shape, hipStream_t stream) {
   switch (shape) {
     case kShapeBig:
-      if constexpr (Q == kNative) return launch_tiles<kForward, Big<kForward, Q>>(p, stream);
+      if constexpr (Q == kNative) return launch_codes<CodesBig<Q>>(p, stream);
       return hipErrorInvalidValue;
-    case kShapeHalf: return launch_tiles<kForward, Half<kForward, Q>>(p, stream);
-    default: return launch_tiles<kForward, Small<kForward, Q>>(p, stream);
+    case kShapeHalf: return launch_codes<CodesHalf<Q>>(p, stream);
+    default: return launch_codes<CodesSmall<Q>>(p, stream);
   }
 }
 
 }  // namespace
+
+bool wants_scales_by_step(const ProductPlan& plan) { return plan.shape == kShapeBig; }
+
+hipError_t launch_scales_by_step(const float* scales, const int32_t* row_ids, int row_div,
+                                 int64_t x_rows, int64_t P, int steps, float* by_step,
+                                 hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((P + kTurnRows - 1) / kTurnRows),
+                  static_cast<unsigned>((steps + kTurnSteps - 1) / kTurnSteps));
+  scales_by_step_kernel<<<grid, 256, 0, stream>>>(scales, row_ids, row_div, x_rows, P, steps,
+                                                  scale_pitch(P), by_step);
+  return hipGetLastError();
+}
 
 hipError_t launch_product_fp8(const ProductArgs& p, const ProductPlan& plan, bool exact,
                               hipStream_t stream) {

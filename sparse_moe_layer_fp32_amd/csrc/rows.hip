@@ -10,6 +10,8 @@
 // formed in fp32 in slot order.  A wave takes 8 columns a lane of one token, 512
 // in all; of narrow rows (up to 256 columns) two, four or eight tokens at once.
 
+#include <type_traits>
+
 #include "activation.h"
 #include "rows.h"
 
@@ -54,7 +56,21 @@ __device__ __forceinline__ void positions(const RowsArgs& p, int64_t token, int 
   }
 }
 
-template <class T, class R, int LANES>
+// STREAM: with the non-temporal hint, on both sides (a constant: accesses that
+// differ in the hint alone are merged without it).
+template <bool STREAM, class E>
+__device__ __forceinline__ F8 get8(const E* p) {
+  return STREAM ? read8(p) : load8(p);
+}
+template <bool STREAM, class E>
+__device__ __forceinline__ void put8(E* p, const F8& v) {
+  if (STREAM)
+    stream8(p, v);
+  else
+    store8(p, v);
+}
+
+template <class T, class R, int LANES, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowsArgs p, int parts) {
   int64_t t;
   int c;
@@ -66,11 +82,11 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowsArgs p, int p
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
       if (at[j] >= 0)
-        store8(static_cast<R*>(p.row_out) + static_cast<int64_t>(at[j]) * p.hidden + c, v);
+        put8<STREAM>(static_cast<R*>(p.row_out) + static_cast<int64_t>(at[j]) * p.hidden + c, v);
   }
 }
 
-template <class T, class R, int LANES>
+template <class T, class R, int LANES, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(RowsArgs p, int parts) {
   int64_t t;
   int c;
@@ -87,7 +103,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(RowsArgs p, i
       w[j] = 1.0f;
       if (at[j] < 0) continue;
       if (p.w) w[j] = p.w[t * p.top_k + j0 + j];
-      v[j] = load8(static_cast<const R*>(p.row) + static_cast<int64_t>(at[j]) * p.hidden + c);
+      v[j] = get8<STREAM>(static_cast<const R*>(p.row) + static_cast<int64_t>(at[j]) * p.hidden + c);
     }
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
@@ -95,55 +111,91 @@ __global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(RowsArgs p, i
 #pragma unroll
         for (int q = 0; q < 8; ++q) sum.v[q] = fmaf(w[j], v[j].v[q], sum.v[q]);
   }
-  store8(static_cast<T*>(p.tok_out) + t * p.hidden + c, sum);
+  put8<STREAM>(static_cast<T*>(p.tok_out) + t * p.hidden + c, sum);
 }
 
-// A block per token (of narrow rows, a wave): the dot products need whole rows.
-// Lanes take columns in turn, their sums meet over the wave and then over the
-// waves in order.
-template <class T, class R, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void combine_grad_kernel(RowsArgs p) {
-  __shared__ float sums[WAVES][kSlots];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = blockIdx.x;
-  for (int j0 = 0; j0 < p.top_k; j0 += kSlots) {
-    int at[kSlots];
-    positions(p, t, j0, at);
-    float w[kSlots], dot[kSlots];
+// SLOTS values of every lane summed over the wave: lane i gets value i % SLOTS.
+// Each exchange halves the values a lane still holds, so that eight values take
+// 10 exchanges and not 48.
+template <int SLOTS>
+__device__ __forceinline__ float wave_sums(const float* v, int lane) {
+  float h[SLOTS];
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
+  for (int i = 0; i < SLOTS; ++i) h[i] = v[i];
+#pragma unroll
+  for (int n = SLOTS / 2; n >= 1; n /= 2) {  // n: the bit of the lane, and values left
+    const bool up = lane & n;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = up ? h[i + n] : h[i], give = up ? h[i] : h[i + n];
+      h[i] = keep + __shfl_xor(give, n);
+    }
+  }
+#pragma unroll
+  for (int off = SLOTS; off < 64; off <<= 1) h[0] += __shfl_xor(h[0], off);
+  return h[0];
+}
+
+// WAVES waves per token: the dot products need whole rows.  Lanes take columns in
+// turn, of all slots' rows at once, and their sums meet over the wave and then
+// over the token's waves in order.  SLOTS: how many of a token's slots are taken
+// together.
+template <class T, class R, int WAVES, int SLOTS, bool STREAM>
+__global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(RowsArgs p) {
+  constexpr int TOKENS = kRowThreads / 64 / WAVES;  // per block
+  __shared__ float sums[TOKENS][WAVES][SLOTS];
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int token = wid / WAVES, wave = wid % WAVES;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * TOKENS + token;
+  const bool live = t < p.tokens;
+  const T* const dy = static_cast<const T*>(p.tok) + t * p.hidden;
+  for (int j0 = 0; j0 < p.top_k; j0 += SLOTS) {
+    int64_t at[SLOTS];  // offset of the slot's row, -1 where there is none
+    float w[SLOTS], dot[SLOTS];
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) {
+      const int64_t i = t * p.top_k + j0 + j;
+      const int v = live && j0 + j < p.top_k ? p.pos[i] : -1;
+      const bool have = v >= 0 && v < p.rows;
+      at[j] = have ? static_cast<int64_t>(v) * p.hidden : -1;
+      w[j] = p.w && have ? p.w[i] : 1.0f;
       dot[j] = 0.0f;
-      w[j] = p.w && at[j] >= 0 ? p.w[t * p.top_k + j0 + j] : 1.0f;
     }
-    for (int c = threadIdx.x * 8; c < p.hidden; c += 64 * WAVES * 8) {
-      const F8 d = load8(static_cast<const T*>(p.tok) + t * p.hidden + c);
+    if (live)
+      for (int c = (wave * 64 + lane) * 8; c < p.hidden; c += 64 * WAVES * 8) {
+        const F8 d = load8(dy + c);
+        F8 r[SLOTS];
+        if (p.dw)
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
-        if (at[j] < 0) continue;
-        const int64_t i = static_cast<int64_t>(at[j]) * p.hidden + c;
-        if (p.dw) {
-          const F8 r = load8(static_cast<const R*>(p.row) + i);
+          for (int j = 0; j < SLOTS; ++j)
+            if (at[j] >= 0) r[j] = get8<STREAM>(static_cast<const R*>(p.row) + at[j] + c);
+        if (p.row_out)
 #pragma unroll
-          for (int q = 0; q < 8; ++q) dot[j] = fmaf(d.v[q], r.v[q], dot[j]);
-        }
-        if (p.row_out) store8(static_cast<R*>(p.row_out) + i, scaled(d, w[j]));
+          for (int j = 0; j < SLOTS; ++j)
+            if (at[j] >= 0)
+              put8<STREAM>(static_cast<R*>(p.row_out) + at[j] + c, scaled(d, w[j]));
+        if (p.dw)
+#pragma unroll
+          for (int j = 0; j < SLOTS; ++j)
+            if (at[j] >= 0)
+#pragma unroll
+              for (int q = 0; q < 8; ++q) dot[j] = fmaf(d.v[q], r[j].v[q], dot[j]);
       }
-    }
     if (!p.dw) continue;
+    float v = wave_sums<SLOTS>(dot, lane);
+    if (WAVES > 1) {
+      if (lane < SLOTS) sums[token][wave][lane] = v;
+      __syncthreads();
+      if (lane < SLOTS) {
+        v = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) dot[j] += __shfl_xor(dot[j], off);
-      if (lane == 0) sums[wave][j] = dot[j];
+        for (int i = 0; i < WAVES; ++i) v += sums[token][i][lane];
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (threadIdx.x < kSlots && j0 + static_cast<int>(threadIdx.x) < p.top_k) {
-      float v = 0.0f;
-#pragma unroll
-      for (int i = 0; i < WAVES; ++i) v += sums[i][threadIdx.x];
-      p.dw[t * p.top_k + j0 + threadIdx.x] = v;
-    }
-    __syncthreads();
+    if (live && wave == 0 && lane < SLOTS && j0 + lane < p.top_k)
+      p.dw[t * p.top_k + j0 + lane] = v;
   }
 }
 
@@ -164,19 +216,41 @@ unsigned row_blocks(const RowsArgs& p, int lanes, int parts) {
   return static_cast<unsigned>((waves + kRowThreads / 64 - 1) / (kRowThreads / 64));
 }
 
-#define MOE_ROWS_LAUNCH(kernel)                                                          \
-  const int lanes = lanes_of(p.hidden), parts = (p.hidden + 511) / 512;                  \
-  const unsigned grid = row_blocks(p, lanes, parts);                                     \
-  with_types(p, [&](auto t, auto r) {                                                    \
-    using T = decltype(t);                                                               \
-    using R = decltype(r);                                                               \
-    switch (lanes) {                                                                     \
-      case 64: kernel<T, R, 64><<<grid, kRowThreads, 0, stream>>>(p, parts); break;      \
-      case 32: kernel<T, R, 32><<<grid, kRowThreads, 0, stream>>>(p, parts); break;      \
-      case 16: kernel<T, R, 16><<<grid, kRowThreads, 0, stream>>>(p, parts); break;      \
-      default: kernel<T, R, 8><<<grid, kRowThreads, 0, stream>>>(p, parts); break;       \
-    }                                                                                    \
-  });                                                                                    \
+// Rows that do not stay in the 256 MB last-level cache between their writer and
+// their reader go past it (8192 x 8 rows of 4096, 537 MB: the sum over slots 109
+// us, from 131, dispatch 108, from 118; 1024 x 8 rows, 67 MB: 17.8, from 14.7).
+bool streams(const RowsArgs& p) {
+  return p.rows * p.hidden * (p.row_f32 ? 4 : 2) > (int64_t(256) << 20);
+}
+
+// Waves per token of the weights' gradient (us with 1 and 4, k = 8: 8192 x 256 20,
+// 57; 8192 x 1024 66, 109; 1024 x 1024 12.3, 11.3; 8192 x 2048 149, 138; 64 x 4096
+// 18.6, 8.6; 8192 x 4096 278, 234).
+int grad_waves(const RowsArgs& p) {
+  return p.hidden > 1024 || (p.hidden > 512 && p.tokens < 4096) ? 4 : 1;
+}
+
+template <class F>
+void with_constant(bool v, F f) {
+  if (v) f(std::true_type{}); else f(std::false_type{});
+}
+
+#define MOE_ROWS_LAUNCH(kernel)                                                               \
+  const int lanes = lanes_of(p.hidden), parts = (p.hidden + 511) / 512;                       \
+  const unsigned grid = row_blocks(p, lanes, parts);                                          \
+  with_types(p, [&](auto t, auto r) {                                                         \
+    using T = decltype(t);                                                                    \
+    using R = decltype(r);                                                                    \
+    with_constant(streams(p), [&](auto s) {                                                   \
+      constexpr bool S = decltype(s)::value;                                                  \
+      switch (lanes) {                                                                        \
+        case 64: kernel<T, R, 64, S><<<grid, kRowThreads, 0, stream>>>(p, parts); break;      \
+        case 32: kernel<T, R, 32, S><<<grid, kRowThreads, 0, stream>>>(p, parts); break;      \
+        case 16: kernel<T, R, 16, S><<<grid, kRowThreads, 0, stream>>>(p, parts); break;      \
+        default: kernel<T, R, 8, S><<<grid, kRowThreads, 0, stream>>>(p, parts); break;       \
+      }                                                                                       \
+    });                                                                                       \
+  });                                                                                         \
   return hipGetLastError()
 
 }  // namespace
@@ -193,14 +267,21 @@ hipError_t launch_combine_rows(const RowsArgs& p, hipStream_t stream) {
 
 hipError_t launch_combine_grad(const RowsArgs& p, hipStream_t stream) {
   if (p.tokens == 0) return hipSuccess;
-  const unsigned grid = static_cast<unsigned>(p.tokens);
+  const int waves = grad_waves(p);
+  const unsigned grid = static_cast<unsigned>((p.tokens * waves + 3) / 4);
   with_types(p, [&](auto t, auto r) {
     using T = decltype(t);
     using R = decltype(r);
-    if (p.hidden <= 512)
-      combine_grad_kernel<T, R, 1><<<grid, 64, 0, stream>>>(p);
-    else
-      combine_grad_kernel<T, R, 4><<<grid, 256, 0, stream>>>(p);
+    with_constant(streams(p), [&](auto s) {
+      constexpr bool S = decltype(s)::value;
+      with_constant(p.top_k <= 4, [&](auto few) {
+        constexpr int N = decltype(few)::value ? 4 : 8;
+        if (waves == 1)
+          combine_grad_kernel<T, R, 1, N, S><<<grid, kRowThreads, 0, stream>>>(p);
+        else
+          combine_grad_kernel<T, R, 4, N, S><<<grid, kRowThreads, 0, stream>>>(p);
+      });
+    });
   });
   return hipGetLastError();
 }
