@@ -13,6 +13,8 @@
 //    there: 128 accumulators, 32 sums, 48 of fragments.)
 #pragma once
 
+#include <algorithm>
+
 #include "product_tile.h"
 
 namespace moe {
@@ -31,36 +33,30 @@ namespace {
 // exact products, fp32 sums, for fp32 results.
 enum CodesKind : int { kNative = 1, kExact = 2 };
 
-// Rings.  SA == SB: both panels SB - 1 steps ahead, and with them the scales of
+// Rings of S stages: both panels S - 1 steps ahead, and with them the scales of
 // the tile's rows, one piece of a wave more per 64 rows (the waves without rows
 // load nothing into a place of their own, so that all count the same loads).
-// SA == SB + 1 (large tiles, all of LDS): a wave holds a step's fragments of W
-// from the step's start, so W's slot is free after a barrier in mid-step, and
-// both panels are two stages ahead; the scales come in registers a step ahead.
-template <int KIND_, int BM_, int BN_, int WM_, int WN_, int SA_, int SB_>
+template <int KIND_, int BM_, int BN_, int WM_, int WN_, int S_>
 struct CodesTile {
-  static constexpr int KIND = KIND_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, SA = SA_, SB = SB_;
+  static constexpr int KIND = KIND_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
   static constexpr int BK = 64;  // in pairs of codes
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr int MB = BM / WM / 32, NB = BN / WN / 32;  // 32 x 32 blocks per wave
   using PA = Panel<BM, BK, false>;
   using PB = Panel<BN, BK, false>;
   static constexpr int JA = PA::PIECES / NW, JB = PB::PIECES / NW;  // pieces per wave and stage
-  static constexpr bool LATE = SA != SB;  // W's slot is free in mid-step
-  static constexpr int AHEAD = LATE ? 2 : SB - 1;
-  static constexpr int RING = SA * PA::BYTES + SB * PB::BYTES;
-  static constexpr int JS = LATE ? 0 : 1;
+  static constexpr int AHEAD = S - 1;
+  static constexpr int RING = S * (PA::BYTES + PB::BYTES);
   static constexpr int SWAVES = BM / 64;
   static constexpr int SBYTES = BM * 4;
-  static constexpr int LDS = RING + (JS ? SA * SBYTES + 256 : 0);
-  static constexpr int J = JA + JB + JS;  // pieces per wave and stage, all told
+  static constexpr int LDS = RING + S * SBYTES + 256;
+  static constexpr int J = JA + JB + 1;  // pieces per wave and stage, all told
   // the fp32 tile leaves in passes that fit the ring
   static constexpr int NEED = (BM * BN * 4 + RING - 1) / RING;
   static constexpr int PASSES = MB % NEED == 0 ? NEED : MB;
   static_assert(MB >= 1 && NB >= 1 && JA >= 1 && JB >= 1 && MB % PASSES == 0 &&
                     BM * BN * 4 / PASSES <= RING && LDS <= 160 * 1024,
                 "tile shape");
-  static_assert(SA == SB || (SA == 3 && SB == 2 && MB >= 3), "ring depths");
   static_assert(AHEAD * J < 64, "vmcnt budget");
   static_assert(BM % 64 == 0 && SWAVES <= NW, "row scales");
   static_assert(128 % (BN / WN) == 0, "a wave's columns share their scale");
@@ -112,7 +108,7 @@ __device__ __forceinline__ void codes_tile(const ProductArgs& p, uint8_t* smem, 
     boff[j] = row < cols ? static_cast<uint32_t>(row) * L * 2 + chunk * 16 : kOutside;
   }
   uint8_t* const aring = smem;
-  uint8_t* const bring = smem + T::SA * PA::BYTES;
+  uint8_t* const bring = smem + T::S * PA::BYTES;
   uint8_t* const sring = smem + T::RING;
   auto records = [&](int kt) MOE_INLINE { return static_cast<int>(kt < k_last ? kRecords : 0u); };
   auto load = [&](const char* base, int kt, uint32_t off, uint8_t* to) MOE_INLINE {
@@ -123,55 +119,36 @@ __device__ __forceinline__ void codes_tile(const ProductArgs& p, uint8_t* smem, 
   auto issue_a = [&](int kt, int j) MOE_INLINE {
     const uint32_t off = (kt == KT - 1 && atail[j]) ? kOutside : aoff[j];
     load(abase, kt, off,
-         aring + ((kt - k_first) % T::SA) * PA::BYTES + (wid * T::JA + j) * 1024);
+         aring + ((kt - k_first) % T::S) * PA::BYTES + (wid * T::JA + j) * 1024);
   };
   auto issue_b = [&](int kt, int j) MOE_INLINE {
     const uint32_t off = (kt == KT - 1 && btail[j]) ? kOutside : boff[j];
     load(bbase, kt, off,
-         bring + ((kt - k_first) % T::SB) * PB::BYTES + (wid * T::JB + j) * 1024);
+         bring + ((kt - k_first) % T::S) * PB::BYTES + (wid * T::JB + j) * 1024);
   };
 
   // ---- scales: of this lane's rows, and of the wave's columns
-  const bool gather = p.src != nullptr && !p.a_scale_ready;
-  const char* const sbase =
-      reinterpret_cast<const char*>(p.a_scale) +
-      (gather ? 0 : static_cast<int64_t>(un.row0) * p.a_scale_row * 4);
-  const int64_t sstep = p.a_scale_step * 4;
+  const char* const sbase = reinterpret_cast<const char*>(
+      p.a_scale + (p.src ? 0 : static_cast<int64_t>(un.row0) * KT));
   auto scale_offset = [&](int row) MOE_INLINE {
     if (row >= un.rows) return kOutside;
-    const int64_t s = gather ? source_row(p, un.row0 + row) : row;
-    return s >= 0 ? static_cast<uint32_t>(s * p.a_scale_row * 4) : kOutside;
+    const int64_t s = p.src ? source_row(p, un.row0 + row) : row;
+    return s >= 0 ? static_cast<uint32_t>(s * KT * 4) : kOutside;
   };
-  uint32_t soff = kOutside;  // equal rings: of the row whose scale this lane fetches
-  uint32_t srow[T::MB];      // late ones: of the rows that it multiplies
-  if constexpr (T::JS) {
-    if (wid < T::SWAVES) soff = scale_offset(64 * wid + lane);
-  } else {
-#pragma unroll
-    for (int mb = 0; mb < T::MB; ++mb)
-      srow[mb] = scale_offset(wm * (T::BM / T::WM) + 32 * mb + (lane & 31));
-  }
+  // of the row whose scale this lane fetches
+  const uint32_t soff = wid < T::SWAVES ? scale_offset(64 * wid + lane) : kOutside;
   const int fblocks = (N + 127) / 128;
   const int fb = min((un.col0 + wn * (T::BN / T::WN)) / 128, fblocks - 1);
   const float* const wscale = p.b_scale + (static_cast<int64_t>(un.g) * fblocks + fb) * KT;
-  float ws_held = 0.0f;     // lane i: the column block's scale of step i of 64
-  float rs_next[T::MB];     // the rows' scales of the step to come
+  float ws_held = 0.0f;  // lane i: the column block's scale of step i of 64
   auto hold_scales = [&](int kt) MOE_INLINE { ws_held = wscale[min(kt + lane, KT - 1)]; };
   auto issue_s = [&](int kt) MOE_INLINE {
     uint8_t* const to = wid < T::SWAVES
-                            ? sring + ((kt - k_first) % T::SA) * T::SBYTES + wid * 256
-                            : sring + T::SA * T::SBYTES;
+                            ? sring + ((kt - k_first) % T::S) * T::SBYTES + wid * 256
+                            : sring + T::S * T::SBYTES;
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(sbase + kt * sstep), 0, records(kt), 0x00027000);
+        const_cast<char*>(sbase + static_cast<int64_t>(kt) * 4), 0, records(kt), 0x00027000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 4, soff, 0, 0, 0);
-  };
-  auto fetch_scales = [&](int kt) MOE_INLINE {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(sbase + kt * sstep), 0, records(kt), 0x00027000);
-#pragma unroll
-    for (int mb = 0; mb < T::MB; ++mb)
-      rs_next[mb] =
-          __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, srow[mb], 0, 0));
   };
 
   // ---- fragments and products
@@ -193,7 +170,7 @@ __device__ __forceinline__ void codes_tile(const ProductArgs& p, uint8_t* smem, 
   // all that a sum over them asks.
   u32x4 bq[T::NB][4], aq[4];
   auto load_b = [&](int kt, int half) MOE_INLINE {
-    uint8_t* sb = bring + ((kt - k_first) % T::SB) * PB::BYTES;
+    uint8_t* sb = bring + ((kt - k_first) % T::S) * PB::BYTES;
 #pragma unroll
     for (int nb = 0; nb < T::NB; ++nb)
 #pragma unroll
@@ -201,7 +178,7 @@ __device__ __forceinline__ void codes_tile(const ProductArgs& p, uint8_t* smem, 
         bq[nb][c] = __builtin_bit_cast(u32x4, PB::frag(sb, bbase_l[nb], c, lane));
   };
   auto load_a = [&](int kt, int mb, int half) MOE_INLINE {
-    uint8_t* sa = aring + ((kt - k_first) % T::SA) * PA::BYTES;
+    uint8_t* sa = aring + ((kt - k_first) % T::S) * PA::BYTES;
 #pragma unroll
     for (int c = 2 * half; c < 2 * half + 2; ++c)
       aq[c] = __builtin_bit_cast(u32x4, PA::frag(sa, abase_l[mb], c, lane));
@@ -234,8 +211,6 @@ __device__ __forceinline__ void codes_tile(const ProductArgs& p, uint8_t* smem, 
     wait_loads<(T::AHEAD - 1) * T::J>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
-  // In mid-step: no wave reads the stage's panel of W any more.
-  auto meet_b = [&]() MOE_INLINE { asm volatile("s_barrier" ::: "memory"); };
   // Piece d of stage kt + AHEAD.
   auto refill = [&](int kt, int d) MOE_INLINE {
     if (d < T::JA)
@@ -247,8 +222,7 @@ __device__ __forceinline__ void codes_tile(const ProductArgs& p, uint8_t* smem, 
   };
 
   if (k_first < k_last) {
-    hold_scales(k_first);  // (these first: the rings' first wait covers them)
-    if constexpr (!T::JS) fetch_scales(k_first);
+    hold_scales(k_first);  // (first: the rings' first wait covers it)
 #pragma unroll
     for (int s = 0; s < T::AHEAD; ++s)
 #pragma unroll
@@ -259,10 +233,7 @@ __device__ __forceinline__ void codes_tile(const ProductArgs& p, uint8_t* smem, 
     if (!has_work) {
       for (int kt = k_first; kt < k_last; ++kt) {
 #pragma unroll
-        for (int d = 0; d < T::J; ++d) {
-          if (T::LATE && d == T::JA) meet_b();
-          refill(kt, d);
-        }
+        for (int d = 0; d < T::J; ++d) refill(kt, d);
         meet();
       }
     } else {
@@ -274,37 +245,24 @@ __device__ __forceinline__ void codes_tile(const ProductArgs& p, uint8_t* smem, 
 #pragma unroll
       for (int nb = 0; nb < T::NB; ++nb) t[nb] = f32x16{};
       auto step = [&](int kt) MOE_INLINE {
-        // Pieces of the refill by row block: late rings x's in the first, before
-        // the barrier, and W's in the others; equal rings evenly, and what is
-        // left in the last one.
+        // Pieces of the refill by row block, and what is left in the last one.
         constexpr int FIRST = T::MB - 1;
-        constexpr int PER = FIRST > 0 ? (T::J + FIRST - 1) / FIRST : 0;
-        constexpr int PERB = FIRST > 1 ? (T::JB + FIRST - 2) / (FIRST - 1) : 0;
+        constexpr int PER = FIRST > 0 ? (T::J + FIRST - 1) / std::max(FIRST, 1) : 0;
         const float w = __builtin_bit_cast(
             float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws_held), (kt - k_first) & 63));
 #pragma unroll
         for (int mb = 0; mb < T::MB; ++mb) {
-          if constexpr (T::JS)
-            rs_next[mb] = *reinterpret_cast<const float*>(
-                sring + ((kt - k_first) % T::SA) * T::SBYTES +
-                (wm * (T::BM / T::WM) + 32 * mb + (lane & 31)) * 4);
-          rs[mb] = rs_next[mb] * w;
+          rs[mb] = w * *reinterpret_cast<const float*>(
+                           sring + ((kt - k_first) % T::S) * T::SBYTES +
+                           (wm * (T::BM / T::WM) + 32 * mb + (lane & 31)) * 4);
         }
-        if (((kt + 1 - k_first) & 63) == 0) {
-          hold_scales(kt + 1);
-          wait_loads<0>();  // (here, so that no other step waits for it)
-        }
-        if constexpr (!T::JS) fetch_scales(kt + 1);
+        if (((kt + 1 - k_first) & 63) == 0) hold_scales(kt + 1);
 #pragma unroll
         for (int mb = 0; mb < T::MB; ++mb) {
           const bool final = mb + 1 == T::MB;
-          if (T::LATE && mb == 0)
-#pragma unroll
-            for (int d = 0; d < T::JA; ++d) refill(kt, d);
           if (final) {
-            if (!T::LATE)
 #pragma unroll
-              for (int d = FIRST * PER; d < T::J; ++d) refill(kt, d);
+            for (int d = FIRST * PER; d < T::J; ++d) refill(kt, d);
             meet();
           }
 #pragma unroll
@@ -323,15 +281,9 @@ __device__ __forceinline__ void codes_tile(const ProductArgs& p, uint8_t* smem, 
               load_b(kt + 1, half);
             }
           }
-          if constexpr (T::LATE) {
-            if (mb == 0) meet_b();  // (the products above have taken all of the panel)
-#pragma unroll
-            for (int d = (mb - 1) * PERB; d < mb * PERB && d < T::JB; ++d)
-              if (mb > 0 && !final) refill(kt, T::JA + d);
-          } else if (!final) {
+          if (!final)
 #pragma unroll
             for (int d = mb * PER; d < (mb + 1) * PER && d < T::J; ++d) refill(kt, d);
-          }
           __builtin_amdgcn_sched_barrier(0);
         }
         last = rs[T::MB - 1];
@@ -352,12 +304,8 @@ __device__ __forceinline__ void codes_tile(const ProductArgs& p, uint8_t* smem, 
   tile_leaves<kForward, T>(p, smem, un, acc, wm, wn);
 }
 
-// Tile shapes, and of the remainders of groups and cut tiles in Big's launches.
-template <int Q> using CodesBig = CodesTile<Q, 256, 256, 2, 4, 3, 2>;
-template <int Q> using CodesThree = CodesTile<Q, 192, 256, 2, 4, 3, 2>;
-template <int Q> using CodesHalf = CodesTile<Q, 128, 256, 2, 4, 3, 3>;
-template <int Q> using CodesFlat = CodesTile<Q, 64, 256, 2, 4, 3, 3>;
-template <int Q> using CodesSmall = CodesTile<Q, 64, 64, 2, 2, 4, 4>;
+template <int Q> using CodesHalf = CodesTile<Q, 128, 256, 2, 4, 3>;
+template <int Q> using CodesSmall = CodesTile<Q, 64, 64, 2, 2, 4>;
 
 }  // namespace
 

@@ -336,7 +336,7 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
 }
 
 // Products of codes: the same tiles over steps of as many bytes, so the same
-// estimates, without Duo, and for fp32 results without Big.
+// estimates, without Duo.  Big: bf16 results of at least two steps in one range.
 ProductPlan product_fp8_plan(int64_t P, int G, int K, int F, int cus, bool exact) {
   const Sizes z = sizes_of(kForward, P, G, K, F);
   if (P <= kThinRows && P * K <= 98304)
@@ -345,11 +345,11 @@ ProductPlan product_fp8_plan(int64_t P, int G, int K, int F, int cus, bool exact
   ProductPlan best{kShapeSmall, 1, cus, 1, 0.0f};
   const bool few = z.ragged && P <= 16 * static_cast<int64_t>(G);
   for (int s : {kShapeBig, kShapeHalf, kShapeSmall}) {
-    if ((exact && s == kShapeBig) || (few && s != kShapeSmall)) continue;
+    if ((s == kShapeBig && (exact || z.steps < 2)) || (few && s != kShapeSmall)) continue;
     const int64_t tiles = few ? tile_count(kForward, P, G, K, F, true, kShapeSizes[s])
                               : tiles_about(kForward, P, G, K, F, s);
     for (int splits = 1; splits <= kFewSplits && splits <= z.steps; splits *= 2) {
-      if (few && splits > 1 && tiles * splits > cus) break;
+      if (splits > 1 && (s == kShapeBig || (few && tiles * splits > cus))) break;
       const int slices =
           s == kShapeBig && !z.ragged && splits == 1 ? last_round_slices(tiles, cus) : 1;
       const float us = product_us(z, tiles, s, splits, slices, cus) +

@@ -166,15 +166,14 @@ moe::ProductArgs map_args(const MapPlan& m, void* ws) {
   return p;
 }
 
-// The forward product of codes, in pairs of them, and its workspace: the scales
-// of x by steps, where the tiles want them so, then partial sums.
+// The forward product of codes, in pairs of them, and its workspace: what its
+// launch prepares, then partial sums.
 struct CodesPlan {
   MapPlan m;
-  bool exact, by_step;
-  int steps;
+  bool exact;
 };
 
-void make_codes_plan(int64_t P, int G, int K, int F, int32_t y_dtype, CodesPlan* c) {
+void make_codes_plan(int64_t P, int G, int K, int F, bool grouped, int32_t y_dtype, CodesPlan* c) {
   c->exact = y_dtype == MOE_DTYPE_F32;
   c->m = MapPlan{};
   c->m.P = P;
@@ -183,9 +182,7 @@ void make_codes_plan(int64_t P, int G, int K, int F, int32_t y_dtype, CodesPlan*
   c->m.F = F;
   c->m.fwd = moe::product_fp8_plan(P, G, K / 2, F, device_cus(), c->exact);
   const size_t part = moe::product_part_bytes(moe::kForward, P, G, K / 2, F, c->m.fwd);
-  c->steps = (K + 127) / 128;
-  c->by_step = moe::wants_scales_by_step(c->m.fwd);
-  c->m.part = c->by_step ? align_up(static_cast<size_t>(moe::scale_pitch(P)) * c->steps * 4) : 0;
+  c->m.part = align_up(moe::codes_prepare_bytes(P, G, K / 2, grouped, c->m.fwd));
   c->m.total = std::max<size_t>(c->m.part + align_up(part), moe::kAlign);
 }
 
@@ -196,23 +193,7 @@ moe::ProductArgs codes_args(const CodesPlan& c, const uint8_t* x, const float* x
   p.b = reinterpret_cast<const uint16_t*>(w);
   p.a_scale = x_scales;
   p.b_scale = w_scales;
-  p.a_scale_row = c.steps;
-  p.a_scale_step = 1;
   return p;
-}
-
-hipError_t forward_codes(const CodesPlan& c, moe::ProductArgs p, void* ws, hipStream_t stream) {
-  if (c.by_step) {
-    float* by_step = at<float>(ws, 0);
-    const hipError_t e = moe::launch_scales_by_step(p.a_scale, p.src, p.row_div, p.x_rows, p.P,
-                                                    c.steps, by_step, stream);
-    if (e != hipSuccess) return e;
-    p.a_scale = by_step;
-    p.a_scale_row = 1;
-    p.a_scale_step = moe::scale_pitch(p.P);
-    p.a_scale_ready = 1;
-  }
-  return moe::launch_product_fp8(p, c.m.fwd, c.exact, stream);
 }
 
 // The input and weight gradients that are wanted of p (with a = dy).
@@ -399,7 +380,7 @@ moe_status moe_swiglu_backward(const moe_swiglu_config* cfg, const uint16_t* dh,
 size_t moe_linear_fp8_workspace_size(const moe_linear_config* cfg) {
   if (validate_linear(cfg) != MOE_OK || check_codes(cfg->in_features) != MOE_OK) return 0;
   CodesPlan c;
-  make_codes_plan(cfg->tokens, 1, cfg->in_features, cfg->out_features, cfg->y_dtype, &c);
+  make_codes_plan(cfg->tokens, 1, cfg->in_features, cfg->out_features, false, cfg->y_dtype, &c);
   return c.m.total;
 }
 
@@ -413,7 +394,7 @@ moe_status moe_linear_forward_fp8(const moe_linear_config* cfg, const uint8_t* x
     return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
   if ((st = check_pointers({x, x_scales, w, w_scales, bias, residual, y, z}))) return st;
   CodesPlan c;
-  make_codes_plan(cfg->tokens, 1, cfg->in_features, cfg->out_features, cfg->y_dtype, &c);
+  make_codes_plan(cfg->tokens, 1, cfg->in_features, cfg->out_features, false, cfg->y_dtype, &c);
   if ((st = check_workspace(c.m.total, ws, ws_bytes))) return st;
   if (cfg->tokens == 0) return ok();
   moe::ProductArgs p = codes_args(c, x, x_scales, w, w_scales, ws);
@@ -423,15 +404,15 @@ moe_status moe_linear_forward_fp8(const moe_linear_config* cfg, const uint8_t* x
   p.y = y;
   p.y_f32 = c.exact;
   p.act = cfg->activation;
-  MOE_CHECK_LAUNCH(forward_codes(c, p, ws, stream), "linear fp8 forward");
+  MOE_CHECK_LAUNCH(moe::launch_product_fp8(p, c.m.fwd, c.exact, ws, stream), "linear fp8 forward");
   return ok();
 }
 
 size_t moe_grouped_fp8_workspace_size(const moe_grouped_config* cfg) {
   if (validate_grouped(cfg) != MOE_OK || check_codes(cfg->in_features) != MOE_OK) return 0;
   CodesPlan c;
-  make_codes_plan(cfg->rows, cfg->num_groups, cfg->in_features, cfg->out_features, cfg->y_dtype,
-                  &c);
+  make_codes_plan(cfg->rows, cfg->num_groups, cfg->in_features, cfg->out_features, true,
+                  cfg->y_dtype, &c);
   return c.m.total;
 }
 
@@ -448,8 +429,8 @@ moe_status moe_grouped_forward_fp8(const moe_grouped_config* cfg, const uint8_t*
   if ((st = check_gather(cfg, row_ids))) return st;
   if ((st = check_pointers({x, x_scales, row_ids, offsets, w, w_scales, bias, y}))) return st;
   CodesPlan c;
-  make_codes_plan(cfg->rows, cfg->num_groups, cfg->in_features, cfg->out_features, cfg->y_dtype,
-                  &c);
+  make_codes_plan(cfg->rows, cfg->num_groups, cfg->in_features, cfg->out_features, true,
+                  cfg->y_dtype, &c);
   if ((st = check_workspace(c.m.total, ws, ws_bytes))) return st;
   if (cfg->rows == 0) return ok();
   moe::ProductArgs p = codes_args(c, x, x_scales, w, w_scales, ws);
@@ -460,7 +441,7 @@ moe_status moe_grouped_forward_fp8(const moe_grouped_config* cfg, const uint8_t*
   p.bias = bias;
   p.y = y;
   p.y_f32 = c.exact;
-  MOE_CHECK_LAUNCH(forward_codes(c, p, ws, stream), "grouped fp8 forward");
+  MOE_CHECK_LAUNCH(moe::launch_product_fp8(p, c.m.fwd, c.exact, ws, stream), "grouped fp8 forward");
   return ok();
 }
 

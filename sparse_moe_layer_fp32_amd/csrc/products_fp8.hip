@@ -7,8 +7,9 @@
 // are one block of codes each.  For bf16 results the tiles multiply codes as they
 // are, for fp32 results codes widened to bf16 (codes_tile.h).
 
-#include "codes_tile.h"
 #include "product_blocks.h"
+
+#include "codes_run.h"
 
 namespace moe {
 
@@ -39,7 +40,7 @@ __global__ __launch_bounds__(64 * kThinWaves) void product_thin_fp8(ProductArgs 
   const uint16_t* x = p.a + max(s, int64_t(0)) * K;
   const int fblocks = (p.F + 127) / 128;
   const float* ws = p.b_scale + (static_cast<int64_t>(un.g) * fblocks + un.col0 / 128) * blocks;
-  const float* xs = p.a_scale + max(s, int64_t(0)) * p.a_scale_row;
+  const float* xs = p.a_scale + max(s, int64_t(0)) * blocks;
   f32x4 acc{};
   for (int c0 = wid; c0 < blocks; c0 += kThinWaves * kThinAhead) {
     u32x4 wf[kThinAhead][2], xf[kThinAhead][2];
@@ -87,30 +88,126 @@ __global__ __launch_bounds__(64 * kThinWaves) void product_thin_fp8(ProductArgs 
              un.col0 + c, p.F);
 }
 
-// A block takes 64 rows and 32 steps through LDS, reading rows and writing steps.
-constexpr int kTurnRows = 64, kTurnSteps = 32;
+// What the large tiles need: x's scales by steps of the rows of y (0 where x has
+// no such row), a block turning 64 rows and 32 steps through LDS; the rows'
+// sources in x; and, of ragged groups, the row tiles, in one block more.
+constexpr int kTurnRows = 64, kTurnSteps = 32, kPrepareThreads = 256;
 
-__global__ __launch_bounds__(256) void scales_by_step_kernel(
+int64_t scale_pitch(int64_t P) { return (P + kTurnRows - 1) / kTurnRows * kTurnRows; }
+
+__device__ void list_row_tiles(const int32_t* __restrict__ offsets, int64_t P, int G,
+                               RowTile* __restrict__ tiles, int32_t* __restrict__ num_tiles,
+                               int* sh) {
+  constexpr int BM = CodesRun::BM;
+  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+  const int c = (G + kPrepareThreads - 1) / kPrepareThreads;
+  auto rows_of = [&](int g, int* begin) {
+    *begin = clamp_row(offsets[g], P);
+    return max(0, clamp_row(offsets[g + 1], P) - *begin);
+  };
+  int mine = 0, b;
+  for (int g = tid * c; g < min(tid * c + c, G); ++g) mine += (rows_of(g, &b) + BM - 1) / BM;
+  int incl = mine;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int o = __shfl_up(incl, off);
+    if (lane >= off) incl += o;
+  }
+  if (lane == 63) sh[wid] = incl;
+  __syncthreads();
+  int at = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPrepareThreads / 64; ++w) {
+    if (w < wid) at += sh[w];
+    total += sh[w];
+  }
+  if (tid == 0) *num_tiles = total;
+  for (int g = tid * c; g < min(tid * c + c, G); ++g) {
+    const int rows = rows_of(g, &b), n = (rows + BM - 1) / BM;
+    for (int i = 0; i < n; ++i)
+      tiles[at + i] = {b + i * BM, min(BM, rows - i * BM), g, at, n, {}};
+    at += n;
+  }
+}
+
+__global__ __launch_bounds__(kPrepareThreads) void codes_prepare_kernel(
     const float* __restrict__ scales, const int32_t* __restrict__ row_ids, int row_div,
-    int64_t x_rows, int64_t P, int steps, int64_t pitch, float* __restrict__ by_step) {
+    int64_t x_rows, int64_t P, int steps, int64_t pitch, float* __restrict__ by_step,
+    const int32_t* __restrict__ offsets, int G, RowTile* __restrict__ tiles,
+    int32_t* __restrict__ num_tiles, uint32_t* __restrict__ sources, uint32_t x_pitch) {
   __shared__ float tile[kTurnSteps][kTurnRows + 1];
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kTurnRows;
+  if (r0 >= P) {  // the block more
+    if (blockIdx.y == 0) list_row_tiles(offsets, P, G, tiles, num_tiles, reinterpret_cast<int*>(tile));
+    return;
+  }
   const int s0 = blockIdx.y * kTurnSteps;
   const int s = threadIdx.x % kTurnSteps;
 #pragma unroll
-  for (int i = threadIdx.x / kTurnSteps; i < kTurnRows; i += 256 / kTurnSteps) {
+  for (int i = threadIdx.x / kTurnSteps; i < kTurnRows; i += kPrepareThreads / kTurnSteps) {
     int64_t src = r0 + i < P ? r0 + i : -1;
     if (src >= 0 && row_ids) {
       const int id = row_ids[src];
       src = id >= 0 && id / row_div < x_rows ? id / row_div : -1;
     }
+    if (row_ids && s == 0 && blockIdx.y == 0)
+      sources[r0 + i] = src >= 0 ? static_cast<uint32_t>(src) * x_pitch : kFar;
     tile[s][i] = src >= 0 && s0 + s < steps ? scales[src * steps + s0 + s] : 0.0f;
   }
   __syncthreads();
   const int r = threadIdx.x % kTurnRows;
 #pragma unroll
-  for (int i = threadIdx.x / kTurnRows; i < kTurnSteps; i += 256 / kTurnRows)
+  for (int i = threadIdx.x / kTurnRows; i < kTurnSteps; i += kPrepareThreads / kTurnRows)
     if (s0 + i < steps) by_step[(s0 + i) * pitch + r0 + r] = tile[i][r];
+}
+
+// The area: the number of row tiles, the tiles, the rows' sources (a tile's more
+// than there are rows), the scales.
+struct CodesArea {
+  size_t tiles, sources, scales, total;
+};
+CodesArea codes_area(int64_t P, int G, int K, bool grouped) {
+  const int64_t tiles = grouped ? P / CodesRun::BM + std::min<int64_t>(G, P) : 0;
+  CodesArea a;
+  a.tiles = 64;
+  a.sources = (a.tiles + tiles * sizeof(RowTile) + 255) / 256 * 256;
+  a.scales = a.sources + (grouped ? (scale_pitch(P) + CodesRun::BM) * 4 : 0);
+  a.total = a.scales + static_cast<size_t>(scale_pitch(P)) * ((K + 63) / 64) * 4;
+  return a;
+}
+
+hipError_t launch_run(ProductArgs p, char* area, hipStream_t stream) {
+  const CodesArea a = codes_area(p.P, p.G, p.K, p.offsets != nullptr);
+  const int steps = (p.K + 63) / 64;
+  const int64_t pitch = scale_pitch(p.P);
+  float* const by_step = reinterpret_cast<float*>(area + a.scales);
+  RowTile* const tiles = p.offsets ? reinterpret_cast<RowTile*>(area + a.tiles) : nullptr;
+  int32_t* const num_tiles = reinterpret_cast<int32_t*>(area);
+  uint32_t* const sources = reinterpret_cast<uint32_t*>(area + a.sources);
+  const dim3 grid(static_cast<unsigned>(pitch / kTurnRows + (tiles ? 1 : 0)),
+                  static_cast<unsigned>((steps + kTurnSteps - 1) / kTurnSteps));
+  codes_prepare_kernel<<<grid, kPrepareThreads, 0, stream>>>(
+      p.a_scale, p.src, p.row_div, p.x_rows, p.P, steps, pitch, by_step, p.offsets, p.G, tiles,
+      num_tiles, sources, static_cast<uint32_t>(p.K) * 2);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  p.a_scale = by_step;
+  p.a_scale_step = pitch;
+  p.tiles = tiles;
+  p.num_tiles = num_tiles;
+  p.sources = sources;
+  // a block of each CU, as many on every XCD, walks the grid of one block per tile
+  const unsigned all = grid_of<kForward, CodesRun>(&p);
+  const unsigned cus = static_cast<unsigned>(std::max(p.cus / kNumXcd * kNumXcd, kNumXcd));
+  const unsigned blocks = std::min(all, cus);
+  const bool act = p.act != MOE_ACT_NONE;
+  if (p.src)  // (a gathered product has no activation)
+    codes_run_kernel<true, false><<<blocks, CodesRun::THREADS, 0, stream>>>(p);
+  else if (act)
+    codes_run_kernel<false, true><<<blocks, CodesRun::THREADS, 0, stream>>>(p);
+  else
+    codes_run_kernel<false, false><<<blocks, CodesRun::THREADS, 0, stream>>>(p);
+  return hipGetLastError();
 }
 
 template <int COLS>
@@ -126,24 +223,9 @@ template <class T>
 __global__ __launch_bounds__(T::THREADS, 2) void codes_kernel(ProductArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
   Unit un;
-  if (!find_unit<kForward, T::BM, T::BN, T::THREADS>(p, blockIdx.x, reinterpret_cast<int*>(smem),
-                                                     &un))
-    return;
-  if constexpr (T::BM == 256) {
-    // fewer rows, the remainder of a group or a cut tile: the same columns with
-    // less of x to load and to multiply
-    using Three = CodesThree<T::KIND>;
-    using Half = CodesHalf<T::KIND>;
-    using Flat = CodesFlat<T::KIND>;
-    static_assert(Flat::LDS <= T::LDS && Half::LDS <= T::LDS && Three::LDS <= T::LDS &&
-                      Flat::THREADS == T::THREADS && Half::THREADS == T::THREADS &&
-                      Three::THREADS == T::THREADS,
-                  "the same LDS and waves");
-    if (un.rows <= 64) return codes_tile<Flat>(p, smem, un);
-    if (un.rows <= 128) return codes_tile<Half>(p, smem, un);
-    if (un.rows <= 192) return codes_tile<Three>(p, smem, un);
-  }
-  codes_tile<T>(p, smem, un);
+  if (find_unit<kForward, T::BM, T::BN, T::THREADS>(p, blockIdx.x, reinterpret_cast<int*>(smem),
+                                                    &un))
+    codes_tile<T>(p, smem, un);
 }
 
 template <class T>
@@ -156,30 +238,17 @@ hipError_t launch_codes(ProductArgs p, hipStream_t stream) {
 
 template <int Q>
 hipError_t launch_shape(const ProductArgs& p, int shape, hipStream_t stream) {
-  switch (shape) {
-    case kShapeBig:
-      if constexpr (Q == kNative) return launch_codes<CodesBig<Q>>(p, stream);
-      return hipErrorInvalidValue;
-    case kShapeHalf: return launch_codes<CodesHalf<Q>>(p, stream);
-    default: return launch_codes<CodesSmall<Q>>(p, stream);
-  }
+  return shape == kShapeHalf ? launch_codes<CodesHalf<Q>>(p, stream)
+                             : launch_codes<CodesSmall<Q>>(p, stream);
 }
 
 }  // namespace
 
-bool wants_scales_by_step(const ProductPlan& plan) { return plan.shape == kShapeBig; }
-
-hipError_t launch_scales_by_step(const float* scales, const int32_t* row_ids, int row_div,
-                                 int64_t x_rows, int64_t P, int steps, float* by_step,
-                                 hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((P + kTurnRows - 1) / kTurnRows),
-                  static_cast<unsigned>((steps + kTurnSteps - 1) / kTurnSteps));
-  scales_by_step_kernel<<<grid, 256, 0, stream>>>(scales, row_ids, row_div, x_rows, P, steps,
-                                                  scale_pitch(P), by_step);
-  return hipGetLastError();
+size_t codes_prepare_bytes(int64_t P, int G, int K, bool grouped, const ProductPlan& plan) {
+  return plan.shape == kShapeBig ? codes_area(P, G, K, grouped).total : 0;
 }
 
-hipError_t launch_product_fp8(const ProductArgs& p, const ProductPlan& plan, bool exact,
+hipError_t launch_product_fp8(const ProductArgs& p, const ProductPlan& plan, bool exact, void* area,
                               hipStream_t stream) {
   ProductArgs q = p;
   q.splits = plan.splits;
@@ -187,6 +256,7 @@ hipError_t launch_product_fp8(const ProductArgs& p, const ProductPlan& plan, boo
   q.slices = plan.slices;
   if (plan.shape == kShapeThin8) return launch_thin_fp8<8>(q, stream);
   if (plan.shape == kShapeThin16) return launch_thin_fp8<16>(q, stream);
+  if (plan.shape == kShapeBig) return launch_run(q, static_cast<char*>(area), stream);
   const hipError_t e = exact ? launch_shape<kExact>(q, plan.shape, stream)
                              : launch_shape<kNative>(q, plan.shape, stream);
   return e != hipSuccess || q.splits == 1 ? e : launch_join<kForward>(q, stream);

@@ -7,8 +7,7 @@
 //
 // Bound: HBM.  All four walk the tokens, so that a token's own row is read or
 // written once, whatever top_k is, and every row of an expert once.  Sums are
-// formed in fp32 in slot order.  A wave takes 8 columns a lane of one token, 512
-// in all; of narrow rows (up to 256 columns) two, four or eight tokens at once.
+// formed in fp32 in slot order.  A lane takes 8 columns of a token.
 
 #include <type_traits>
 
@@ -29,20 +28,21 @@ __device__ __forceinline__ F8 scaled(const F8& v, float w) {
   return o;
 }
 
-// The token and first column of this lane; false if there is none.  LANES: how
-// many lanes a token has in a wave.
-template <int LANES>
-__device__ __forceinline__ bool locate(const RowsArgs& p, int parts, int64_t* token, int* col) {
-  const int lane = threadIdx.x & 63;
-  const uint32_t wave = blockIdx.x * (kRowThreads / 64) +
-                        __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (LANES == 64) {
+// The token and first column of this lane; false if there is none.  WHOLE: a wave
+// has one token; else lanes take the chunks of all tokens one after the other.
+template <bool WHOLE>
+__device__ __forceinline__ bool locate(const RowsArgs& p, uint32_t parts, int64_t* token, int* col) {
+  if (WHOLE) {
+    const uint32_t wave = blockIdx.x * (kRowThreads / 64) +
+                          __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t t = wave / parts;
     *token = t;
-    *col = static_cast<int>((wave - t * parts) * 64 + lane) * 8;
+    *col = static_cast<int>((wave - t * parts) * 64 + (threadIdx.x & 63)) * 8;
   } else {
-    *token = static_cast<int64_t>(wave) * (64 / LANES) + lane / LANES;
-    *col = lane % LANES * 8;
+    const uint32_t chunk = blockIdx.x * kRowThreads + threadIdx.x;
+    const uint32_t t = chunk / parts;
+    *token = t;
+    *col = static_cast<int>(chunk - t * parts) * 8;
   }
   return *token < p.tokens && *col < p.hidden;
 }
@@ -70,11 +70,11 @@ __device__ __forceinline__ void put8(E* p, const F8& v) {
     store8(p, v);
 }
 
-template <class T, class R, int LANES, bool STREAM>
-__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowsArgs p, int parts) {
+template <class T, class R, bool WHOLE, bool STREAM>
+__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowsArgs p, uint32_t parts) {
   int64_t t;
   int c;
-  if (!locate<LANES>(p, parts, &t, &c)) return;
+  if (!locate<WHOLE>(p, parts, &t, &c)) return;
   const F8 v = load8(static_cast<const T*>(p.tok) + t * p.hidden + c);
   for (int j0 = 0; j0 < p.top_k; j0 += kSlots) {
     int at[kSlots];
@@ -86,11 +86,11 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(RowsArgs p, int p
   }
 }
 
-template <class T, class R, int LANES, bool STREAM>
-__global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(RowsArgs p, int parts) {
+template <class T, class R, bool WHOLE, bool STREAM>
+__global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(RowsArgs p, uint32_t parts) {
   int64_t t;
   int c;
-  if (!locate<LANES>(p, parts, &t, &c)) return;
+  if (!locate<WHOLE>(p, parts, &t, &c)) return;
   F8 sum{};
   if (p.base) sum = load8(static_cast<const T*>(p.base) + t * p.hidden + c);
   for (int j0 = 0; j0 < p.top_k; j0 += kSlots) {
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(RowsArgs p) {
   }
 }
 
-// One of the four pairs of types, and the lanes a token has.
+// One of the four pairs of types.
 template <class F>
 void with_types(const RowsArgs& p, F f) {
   if (p.tok_f32) {
@@ -207,13 +207,6 @@ void with_types(const RowsArgs& p, F f) {
   } else {
     if (p.row_f32) f(uint16_t{}, float{}); else f(uint16_t{}, uint16_t{});
   }
-}
-
-int lanes_of(int hidden) { return hidden > 256 ? 64 : hidden > 128 ? 32 : hidden > 64 ? 16 : 8; }
-
-unsigned row_blocks(const RowsArgs& p, int lanes, int parts) {
-  const int64_t waves = lanes == 64 ? p.tokens * parts : (p.tokens * lanes + 63) / 64;
-  return static_cast<unsigned>((waves + kRowThreads / 64 - 1) / (kRowThreads / 64));
 }
 
 // Rows that do not stay in the 256 MB last-level cache between their writer and
@@ -235,22 +228,23 @@ void with_constant(bool v, F f) {
   if (v) f(std::true_type{}); else f(std::false_type{});
 }
 
-#define MOE_ROWS_LAUNCH(kernel)                                                               \
-  const int lanes = lanes_of(p.hidden), parts = (p.hidden + 511) / 512;                       \
-  const unsigned grid = row_blocks(p, lanes, parts);                                          \
-  with_types(p, [&](auto t, auto r) {                                                         \
-    using T = decltype(t);                                                                    \
-    using R = decltype(r);                                                                    \
-    with_constant(streams(p), [&](auto s) {                                                   \
-      constexpr bool S = decltype(s)::value;                                                  \
-      switch (lanes) {                                                                        \
-        case 64: kernel<T, R, 64, S><<<grid, kRowThreads, 0, stream>>>(p, parts); break;      \
-        case 32: kernel<T, R, 32, S><<<grid, kRowThreads, 0, stream>>>(p, parts); break;      \
-        case 16: kernel<T, R, 16, S><<<grid, kRowThreads, 0, stream>>>(p, parts); break;      \
-        default: kernel<T, R, 8, S><<<grid, kRowThreads, 0, stream>>>(p, parts); break;       \
-      }                                                                                       \
-    });                                                                                       \
-  });                                                                                         \
+// Waves of one token each, or of narrow rows lanes packed.
+#define MOE_ROWS_LAUNCH(kernel)                                                                 \
+  const bool whole = p.hidden >= 512;                                                           \
+  const int parts = whole ? (p.hidden + 511) / 512 : p.hidden / 8;                              \
+  const int64_t threads = p.tokens * parts * (whole ? 64 : 1);                                  \
+  const unsigned grid = static_cast<unsigned>((threads + kRowThreads - 1) / kRowThreads);       \
+  with_types(p, [&](auto t, auto r) {                                                           \
+    using T = decltype(t);                                                                      \
+    using R = decltype(r);                                                                      \
+    with_constant(streams(p), [&](auto s) {                                                     \
+      constexpr bool S = decltype(s)::value;                                                    \
+      if (whole)                                                                                \
+        kernel<T, R, true, S><<<grid, kRowThreads, 0, stream>>>(p, parts);                      \
+      else                                                                                      \
+        kernel<T, R, false, S><<<grid, kRowThreads, 0, stream>>>(p, parts);                     \
+    });                                                                                         \
+  });                                                                                           \
   return hipGetLastError()
 
 }  // namespace
