@@ -335,28 +335,79 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
   return best;
 }
 
-// Products of codes: the same tiles over steps of as many bytes, so the same
-// estimates, without Duo.  Big: bf16 results of at least two steps in one range.
-ProductPlan product_fp8_plan(int64_t P, int G, int K, int F, int cus, bool exact) {
-  const Sizes z = sizes_of(kForward, P, G, K, F);
-  if (P <= kThinRows && P * K <= 98304)
-    return {tiles_about(kForward, P, G, K, F, kShapeThin16) <= cus / 2 ? kShapeThin8 : kShapeThin16,
-            1, cus, 1, 0.0f};
-  ProductPlan best{kShapeSmall, 1, cus, 1, 0.0f};
-  const bool few = z.ragged && P <= 16 * static_cast<int64_t>(G);
-  for (int s : {kShapeBig, kShapeHalf, kShapeSmall}) {
-    if ((s == kShapeBig && (exact || z.steps < 2)) || (few && s != kShapeSmall)) continue;
-    const int64_t tiles = few ? tile_count(kForward, P, G, K, F, true, kShapeSizes[s])
-                              : tiles_about(kForward, P, G, K, F, s);
-    for (int splits = 1; splits <= kFewSplits && splits <= z.steps; splits *= 2) {
-      if (splits > 1 && (s == kShapeBig || (few && tiles * splits > cus))) break;
-      const int slices =
-          s == kShapeBig && !z.ragged && splits == 1 ? last_round_slices(tiles, cus) : 1;
-      const float us = product_us(z, tiles, s, splits, slices, cus) +
-                       (few && splits > 1 ? kRaggedJoin : 0.0f);
-      if (best.us == 0.0f || us < best.us) best = {s, splits, cus, slices, us};
-    }
+// Products of codes: the same estimate from figures of their own, fitted to the
+// times of 2123 products (2 to 16384 rows, 64 to 11264 features, 1 to 288 groups,
+// bf16 and fp32 results) in every shape and split: the choice is 2% slower than
+// the best measured on the mean; by the figures of the bf16 products it was 4.5%.
+// Steps are of 128 codes, of the thin kernel 4096.  `share`: tiles that a group
+// with rows has more, as a part of one.  Big (with its prepare launch: kPrepare):
+// bf16 results, in one range, of two steps or more.
+struct CodesCost {
+  int per_cu;
+  float full, partly, fixed, share;
+};
+constexpr CodesCost kCodesNative[] = {{1, 1.90f, 1.21f, 10.8f, 1 / 5.2f},
+                                      {1, 2.25f, 0.665f, 6.7f, 1 / 2.3f},
+                                      {},
+                                      {2, 0.549f, 0.145f, 5.3f, 1 / 1.8f}};
+constexpr CodesCost kCodesExact[] = {{},
+                                     {1, 1.30f, 0.66f, 6.0f, 1 / 2.3f},
+                                     {},
+                                     {2, 0.50f, 0.219f, 2.5f, 1 / 1.8f}};
+constexpr CodesCost kCodesThin = {2, 3.64f, 0.69f, 2.35f, 1 / 0.85f};
+constexpr float kCodesFilling = 0.87f, kCodesJoin = 2.5f, kCodesJoinBytesPerUs = 6.1e6f;
+constexpr float kPrepare = 10.4f;
+constexpr int64_t kCodesThinRows = 64;
+
+namespace {
+
+float codes_us(const CodesCost& c, int64_t P, int G, int F, int64_t steps, ShapeSize size,
+               int splits, int cus) {
+  float rows = static_cast<float>((P + size.bm - 1) / size.bm);
+  if (G > 1) rows += static_cast<float>(std::min<int64_t>(G, P) + 1) * c.share;
+  const float units = rows * static_cast<float>((F + size.bn - 1) / size.bn) * splits;
+  const float slots = static_cast<float>(cus) * c.per_cu;
+  const float n = static_cast<float>((steps + splits - 1) / splits);
+  const float whole = n * c.full + c.fixed;
+  float us;
+  if (G > 1 && units > slots) {  // tiles of different lengths end at different times
+    us = units / slots * whole;
+  } else {
+    const float rounds = static_cast<float>(static_cast<int64_t>(units / slots));
+    const float rest = units - rounds * slots;
+    us = rounds * whole;
+    if (rest > cus)
+      us += whole;
+    else if (rest > 0.0f)
+      us += n * c.partly * (1.0f + kCodesFilling * rest / cus) + c.fixed;
   }
+  if (splits > 1)
+    us += kCodesJoin + (G > 1 ? kRaggedJoin : 0.0f) +
+          static_cast<float>(P) * F * (8.0f * splits + 4.0f) / kCodesJoinBytesPerUs;
+  return us;
+}
+
+}  // namespace
+
+ProductPlan product_fp8_plan(int64_t P, int G, int K, int F, int cus, bool exact) {
+  const int64_t steps = (K + 63) / 64;
+  ProductPlan best{kShapeSmall, 1, cus, 1, 0.0f};
+  auto consider = [&](int shape, int splits, float us) {
+    if (best.us == 0.0f || us < best.us) best = {shape, splits, cus, 1, us};
+  };
+  if (P <= kCodesThinRows)
+    for (int s : {kShapeThin8, kShapeThin16})
+      consider(s, 1, codes_us(kCodesThin, P, G, F, (steps + 31) / 32, kShapeSizes[s], 1, cus));
+  if (!exact && steps >= 2)
+    consider(kShapeBig, 1, kPrepare + codes_us(kCodesNative[kShapeBig], P, G, F, steps,
+                                               kShapeSizes[kShapeBig], 1, cus));
+  for (int s : {kShapeHalf, kShapeSmall})
+    for (int splits = 1; splits <= kFewSplits && splits <= steps; splits *= 2)
+      consider(s, splits, codes_us((exact ? kCodesExact : kCodesNative)[s], P, G, F, steps,
+                                   kShapeSizes[s], splits, cus));
+  if (best.shape == kShapeBig && G == 1)
+    best.slices = last_round_slices(tile_count(kForward, P, 1, K, F, false, kShapeSizes[kShapeBig]),
+                                    cus);
   return best;
 }
 
