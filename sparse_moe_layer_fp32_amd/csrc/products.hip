@@ -336,27 +336,30 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
 }
 
 // Products of codes: the same estimate from figures of their own, fitted to the
-// times of 2123 products (2 to 16384 rows, 64 to 11264 features, 1 to 288 groups,
-// bf16 and fp32 results) in every shape and split: the choice is 2% slower than
+// times of 2140 products (2 to 16384 rows, 64 to 11264 features, 1 to 288 groups,
+// bf16 and fp32 results) in every shape and split: the choice is 1.7% slower than
 // the best measured on the mean; by the figures of the bf16 products it was 4.5%.
-// Steps are of 128 codes, of the thin kernel 4096.  `share`: tiles that a group
-// with rows has more, as a part of one.  Big (with its prepare launch: kPrepare):
-// bf16 results, in one range, of two steps or more.
+// Steps are of 128 codes, of the thin kernel 4096.  `share`: the least part of a
+// tile that a group with rows has more than its rows fill.  No shape is faster
+// than the stream of its weights; of those that it bounds the one with the least
+// work is taken (512 rows in 288 groups, 4096 -> 1280: 143 us in Half or Small,
+// 153 in Big).  Big (with its prepare launch: kPrepare): bf16 results, in one
+// range, of two steps or more.
 struct CodesCost {
   int per_cu;
   float full, partly, fixed, share;
 };
-constexpr CodesCost kCodesNative[] = {{1, 1.90f, 1.21f, 10.8f, 1 / 5.2f},
-                                      {1, 2.25f, 0.665f, 6.7f, 1 / 2.3f},
+constexpr CodesCost kCodesNative[] = {{1, 1.376f, 0.782f, 5.0f, 0.485f},
+                                      {1, 1.159f, 0.535f, 6.9f, 0.624f},
                                       {},
-                                      {2, 0.549f, 0.145f, 5.3f, 1 / 1.8f}};
+                                      {2, 0.442f, 0.140f, 5.7f, 0.826f}};
 constexpr CodesCost kCodesExact[] = {{},
-                                     {1, 1.30f, 0.66f, 6.0f, 1 / 2.3f},
+                                     {1, 1.368f, 0.989f, 6.3f, 0.624f},
                                      {},
-                                     {2, 0.50f, 0.219f, 2.5f, 1 / 1.8f}};
-constexpr CodesCost kCodesThin = {2, 3.64f, 0.69f, 2.35f, 1 / 0.85f};
-constexpr float kCodesFilling = 0.87f, kCodesJoin = 2.5f, kCodesJoinBytesPerUs = 6.1e6f;
-constexpr float kPrepare = 10.4f;
+                                     {2, 0.525f, 0.202f, 5.4f, 0.826f}};
+constexpr CodesCost kCodesThin = {1, 2.685f, 0.337f, 2.46f, 0.334f};
+constexpr float kCodesFilling = 0.79f, kCodesJoin = 2.0f, kCodesJoinBytesPerUs = 11.5e6f;
+constexpr float kPrepare = 3.4f, kCodesBytesPerUs = 4.8e6f, kCodesBeyond = 0.105f;
 constexpr int64_t kCodesThinRows = 64;
 
 namespace {
@@ -364,7 +367,11 @@ namespace {
 float codes_us(const CodesCost& c, int64_t P, int G, int F, int64_t steps, ShapeSize size,
                int splits, int cus) {
   float rows = static_cast<float>((P + size.bm - 1) / size.bm);
-  if (G > 1) rows += static_cast<float>(std::min<int64_t>(G, P) + 1) * c.share;
+  if (G > 1) {
+    const float filled = static_cast<float>(P) / size.bm;
+    const float groups = static_cast<float>(std::min<int64_t>(G, P));
+    rows = filled + std::max(groups * c.share, groups - filled);
+  }
   const float units = rows * static_cast<float>((F + size.bn - 1) / size.bn) * splits;
   const float slots = static_cast<float>(cus) * c.per_cu;
   const float n = static_cast<float>((steps + splits - 1) / splits);
@@ -392,7 +399,10 @@ float codes_us(const CodesCost& c, int64_t P, int G, int F, int64_t steps, Shape
 ProductPlan product_fp8_plan(int64_t P, int G, int K, int F, int cus, bool exact) {
   const int64_t steps = (K + 63) / 64;
   ProductPlan best{kShapeSmall, 1, cus, 1, 0.0f};
+  const float weights =  // K counts pairs of codes
+      static_cast<float>(std::min<int64_t>(G, P)) * F * 2.0f * K / kCodesBytesPerUs;
   auto consider = [&](int shape, int splits, float us) {
+    us = std::max(us, weights) + kCodesBeyond * us;
     if (best.us == 0.0f || us < best.us) best = {shape, splits, cus, 1, us};
   };
   if (P <= kCodesThinRows)
