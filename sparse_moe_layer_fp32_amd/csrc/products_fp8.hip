@@ -96,8 +96,8 @@ constexpr int kTurnRows = 64, kTurnSteps = 32, kPrepareThreads = 256;
 int64_t scale_pitch(int64_t P) { return (P + kTurnRows - 1) / kTurnRows * kTurnRows; }
 
 __device__ void list_row_tiles(const int32_t* __restrict__ offsets, int64_t P, int G,
-                               RowTile* __restrict__ tiles, int32_t* __restrict__ num_tiles,
-                               int* sh) {
+                               RowTile* __restrict__ tiles, int most,
+                               int32_t* __restrict__ num_tiles, int* sh) {
   constexpr int BM = CodesRun::BM;
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
   const int c = (G + kPrepareThreads - 1) / kPrepareThreads;
@@ -121,9 +121,11 @@ __device__ void list_row_tiles(const int32_t* __restrict__ offsets, int64_t P, i
     if (w < wid) at += sh[w];
     total += sh[w];
   }
-  if (tid == 0) *num_tiles = total;
+  if (tid == 0) *num_tiles = min(total, most);
   for (int g = tid * c; g < min(tid * c + c, G); ++g) {
-    const int rows = rows_of(g, &b), n = (rows + BM - 1) / BM;
+    const int rows = rows_of(g, &b);
+    // (offsets that do not ascend could make more tiles than there is room for)
+    const int n = min((rows + BM - 1) / BM, max(0, most - at));
     for (int i = 0; i < n; ++i)
       tiles[at + i] = {b + i * BM, min(BM, rows - i * BM), g, at, n, {}};
     at += n;
@@ -133,12 +135,13 @@ __device__ void list_row_tiles(const int32_t* __restrict__ offsets, int64_t P, i
 __global__ __launch_bounds__(kPrepareThreads) void codes_prepare_kernel(
     const float* __restrict__ scales, const int32_t* __restrict__ row_ids, int row_div,
     int64_t x_rows, int64_t P, int steps, int64_t pitch, float* __restrict__ by_step,
-    const int32_t* __restrict__ offsets, int G, RowTile* __restrict__ tiles,
+    const int32_t* __restrict__ offsets, int G, RowTile* __restrict__ tiles, int most_tiles,
     int32_t* __restrict__ num_tiles, uint32_t* __restrict__ sources, uint32_t x_pitch) {
   __shared__ float tile[kTurnSteps][kTurnRows + 1];
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kTurnRows;
   if (r0 >= P) {  // the block more
-    if (blockIdx.y == 0) list_row_tiles(offsets, P, G, tiles, num_tiles, reinterpret_cast<int*>(tile));
+    if (blockIdx.y == 0)
+      list_row_tiles(offsets, P, G, tiles, most_tiles, num_tiles, reinterpret_cast<int*>(tile));
     return;
   }
   const int s0 = blockIdx.y * kTurnSteps;
@@ -165,11 +168,13 @@ __global__ __launch_bounds__(kPrepareThreads) void codes_prepare_kernel(
 // than there are rows), the scales.
 struct CodesArea {
   size_t tiles, sources, scales, total;
+  int most_tiles;
 };
 CodesArea codes_area(int64_t P, int G, int K, bool grouped) {
   const int64_t tiles = grouped ? P / CodesRun::BM + std::min<int64_t>(G, P) : 0;
   CodesArea a;
   a.tiles = 64;
+  a.most_tiles = static_cast<int>(tiles);
   a.sources = (a.tiles + tiles * sizeof(RowTile) + 255) / 256 * 256;
   a.scales = a.sources + (grouped ? (scale_pitch(P) + CodesRun::BM) * 4 : 0);
   a.total = a.scales + static_cast<size_t>(scale_pitch(P)) * ((K + 63) / 64) * 4;
@@ -188,7 +193,7 @@ hipError_t launch_run(ProductArgs p, char* area, hipStream_t stream) {
                   static_cast<unsigned>((steps + kTurnSteps - 1) / kTurnSteps));
   codes_prepare_kernel<<<grid, kPrepareThreads, 0, stream>>>(
       p.a_scale, p.src, p.row_div, p.x_rows, p.P, steps, pitch, by_step, p.offsets, p.G, tiles,
-      num_tiles, sources, static_cast<uint32_t>(p.K) * 2);
+      a.most_tiles, num_tiles, sources, static_cast<uint32_t>(p.K) * 2);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   p.a_scale = by_step;
