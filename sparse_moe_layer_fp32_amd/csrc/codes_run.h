@@ -56,7 +56,7 @@ struct Walk {
   int NT, units, cut;   // column tiles; tiles; dense: the first that is cut, or -1
 };
 
-__device__ __forceinline__ Walk start_walk(const ProductArgs& p) {
+__device__ __forceinline__ Walk start_walk(const CodesArgs& p) {
   Walk w;
   w.bid = blockIdx.x;
   w.NT = (p.F + CodesRun::BN - 1) / CodesRun::BN;
@@ -68,7 +68,7 @@ __device__ __forceinline__ Walk start_walk(const ProductArgs& p) {
   return w;
 }
 
-__device__ __forceinline__ bool next_tile(const ProductArgs& p, Walk* w, Unit* un) {
+__device__ __forceinline__ bool next_tile(const CodesArgs& p, Walk* w, Unit* un) {
   for (; w->bid < w->limit; w->bid += gridDim.x) {
     int part = 0, parts = 1;
     const int v = w->cut >= 0 ? cut_unit(w->bid, w->cut, w->units, p.slices, &part)
@@ -117,7 +117,7 @@ __device__ __forceinline__ void split_rows(float v, float* lo, float* hi) {
 
 // GATHER: x's rows are named by p.src.  ACT: there is an activation.
 template <bool GATHER, bool ACT>
-__global__ __launch_bounds__(CodesRun::THREADS, 2) void codes_run_kernel(ProductArgs p) {
+__global__ __launch_bounds__(CodesRun::THREADS, 2) void codes_run_kernel(CodesArgs p) {
   using R = CodesRun;
   using Pan = R::Pan;
   typedef int i32x8 __attribute__((ext_vector_type(8)));

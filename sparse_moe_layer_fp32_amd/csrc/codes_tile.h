@@ -63,7 +63,7 @@ struct CodesTile {
 };
 
 template <class T>
-__device__ __forceinline__ void codes_tile(const ProductArgs& p, uint8_t* smem, const Unit& un) {
+__device__ __forceinline__ void codes_tile(const CodesArgs& p, uint8_t* smem, const Unit& un) {
   using PA = typename T::PA;
   using PB = typename T::PB;
   typedef int i32x8 __attribute__((ext_vector_type(8)));

@@ -15,13 +15,6 @@ enum ProductOp : int {
   kWeightGrad = 2  // dW[f][k] = sum_r dy[r][f] x[src(r)][k],  db[f] = sum_r dy[r][f]
 };
 
-// A row tile of a ragged product of codes.
-struct RowTile {
-  int32_t row0, rows, g;
-  int32_t first, tiles;  // of its group: the first tile's index, and their number
-  int32_t pad[3];
-};
-
 // Arguments of one product.  Rows [offsets[g], offsets[g+1]) belong to group
 // g; a null `offsets` means one group of all P rows.  Offsets are clamped to
 // [0, P] on the device.
@@ -50,18 +43,28 @@ struct ProductArgs {
   int splits;
   float* part;
   float* part_db;
-  // e4m3 codes (forward): a and b as rows of K 16-bit pairs of codes, and their
-  // scales: a's of a step and row at [row of x][step] (codes_run: a_scale[step
-  // a_scale_step + row of y]), b's at [G][F / 128][step], rounded up.
-  const float* a_scale;
-  const float* b_scale;
-  int64_t a_scale_step;
-  const struct RowTile* tiles;  // codes_run with groups: row tiles, and their number
-  const int32_t* num_tiles;
-  const uint32_t* sources;  // codes_run with src: byte offsets of the rows of y in x
   // set by the launcher
   int cus;
   int whole, slices;  // Big tiles left whole (-1: all), slices of the rows of the others
+};
+
+// A row tile of a ragged product of codes.
+struct RowTile {
+  int32_t row0, rows, g;
+  int32_t first, tiles;  // of its group: the first tile's index, and their number
+  int32_t pad[3];
+};
+
+// Arguments of one product of e4m3 codes: a and b as rows of K 16-bit pairs of
+// codes, and their scales: a's of a step and row at [row of x][step] (codes_run:
+// a_scale[step a_scale_step + row of y]), b's at [G][F / 128][step], rounded up.
+struct CodesArgs : ProductArgs {
+  const float* a_scale;
+  const float* b_scale;
+  int64_t a_scale_step;
+  const RowTile* tiles;  // codes_run with groups: row tiles, and their number
+  const int32_t* num_tiles;
+  const uint32_t* sources;  // codes_run with src: byte offsets of the rows of y in x
 };
 
 // How a product is run: the tile shape and the number of contraction ranges.
@@ -82,7 +85,7 @@ ProductPlan product_fp8_plan(int64_t P, int G, int K, int F, int cus, bool exact
 // tiles the row tiles and x's scales by step.
 size_t codes_prepare_bytes(int64_t P, int G, int K, bool grouped, const ProductPlan& plan);
 // `area`: that many bytes.
-hipError_t launch_product_fp8(const ProductArgs& p, const ProductPlan& plan, bool exact, void* area,
+hipError_t launch_product_fp8(const CodesArgs& p, const ProductPlan& plan, bool exact, void* area,
                               hipStream_t stream);
 // Bytes of `part` (with part_db behind it) for that plan; 0 when splits == 1.
 size_t product_part_bytes(int op, int64_t P, int G, int K, int F, const ProductPlan& plan);

@@ -186,9 +186,9 @@ void make_codes_plan(int64_t P, int G, int K, int F, bool grouped, int32_t y_dty
   c->m.total = std::max<size_t>(c->m.part + align_up(part), moe::kAlign);
 }
 
-moe::ProductArgs codes_args(const CodesPlan& c, const uint8_t* x, const float* x_scales,
-                            const uint8_t* w, const float* w_scales, void* ws) {
-  moe::ProductArgs p = map_args(c.m, ws);
+moe::CodesArgs codes_args(const CodesPlan& c, const uint8_t* x, const float* x_scales,
+                          const uint8_t* w, const float* w_scales, void* ws) {
+  moe::CodesArgs p{map_args(c.m, ws)};
   p.a = reinterpret_cast<const uint16_t*>(x);
   p.b = reinterpret_cast<const uint16_t*>(w);
   p.a_scale = x_scales;
@@ -397,7 +397,7 @@ moe_status moe_linear_forward_fp8(const moe_linear_config* cfg, const uint8_t* x
   make_codes_plan(cfg->tokens, 1, cfg->in_features, cfg->out_features, false, cfg->y_dtype, &c);
   if ((st = check_workspace(c.m.total, ws, ws_bytes))) return st;
   if (cfg->tokens == 0) return ok();
-  moe::ProductArgs p = codes_args(c, x, x_scales, w, w_scales, ws);
+  moe::CodesArgs p = codes_args(c, x, x_scales, w, w_scales, ws);
   p.bias = bias;
   p.residual = residual;
   p.z = z;
@@ -433,7 +433,7 @@ moe_status moe_grouped_forward_fp8(const moe_grouped_config* cfg, const uint8_t*
                   cfg->y_dtype, &c);
   if ((st = check_workspace(c.m.total, ws, ws_bytes))) return st;
   if (cfg->rows == 0) return ok();
-  moe::ProductArgs p = codes_args(c, x, x_scales, w, w_scales, ws);
+  moe::CodesArgs p = codes_args(c, x, x_scales, w, w_scales, ws);
   p.offsets = offsets;
   p.src = row_ids;
   p.row_div = cfg->row_div;

@@ -24,7 +24,7 @@ constexpr int kThinWaves = 8;
 constexpr int kThinAhead = 4;  // blocks that a wave requests before it multiplies
 
 template <int COLS>
-__global__ __launch_bounds__(64 * kThinWaves) void product_thin_fp8(ProductArgs p) {
+__global__ __launch_bounds__(64 * kThinWaves) void product_thin_fp8(CodesArgs p) {
   __shared__ __attribute__((aligned(16))) float sums[kThinWaves * 256];
   Unit un;
   if (!find_unit<kForward, kThinRows, COLS, 64 * kThinWaves>(p, blockIdx.x,
@@ -181,7 +181,7 @@ CodesArea codes_area(int64_t P, int G, int K, bool grouped) {
   return a;
 }
 
-hipError_t launch_run(ProductArgs p, char* area, hipStream_t stream) {
+hipError_t launch_run(CodesArgs p, char* area, hipStream_t stream) {
   const CodesArea a = codes_area(p.P, p.G, p.K, p.offsets != nullptr);
   const int steps = (p.K + 63) / 64;
   const int64_t pitch = scale_pitch(p.P);
@@ -216,7 +216,7 @@ hipError_t launch_run(ProductArgs p, char* area, hipStream_t stream) {
 }
 
 template <int COLS>
-hipError_t launch_thin_fp8(const ProductArgs& p, hipStream_t stream) {
+hipError_t launch_thin_fp8(const CodesArgs& p, hipStream_t stream) {
   const int64_t units =
       tile_count(kForward, p.P, p.G, p.K, p.F, p.offsets != nullptr, {kThinRows, COLS});
   if (units <= 0) return hipSuccess;
@@ -225,7 +225,7 @@ hipError_t launch_thin_fp8(const ProductArgs& p, hipStream_t stream) {
 }
 
 template <class T>
-__global__ __launch_bounds__(T::THREADS, 2) void codes_kernel(ProductArgs p) {
+__global__ __launch_bounds__(T::THREADS, 2) void codes_kernel(CodesArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
   Unit un;
   if (find_unit<kForward, T::BM, T::BN, T::THREADS>(p, blockIdx.x, reinterpret_cast<int*>(smem),
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void codes_kernel(ProductArgs p) {
 }
 
 template <class T>
-hipError_t launch_codes(ProductArgs p, hipStream_t stream) {
+hipError_t launch_codes(CodesArgs p, hipStream_t stream) {
   const unsigned grid = grid_of<kForward, T>(&p);
   if (grid == 0) return hipSuccess;
   codes_kernel<T><<<grid, T::THREADS, 0, stream>>>(p);
@@ -242,7 +242,7 @@ hipError_t launch_codes(ProductArgs p, hipStream_t stream) {
 }
 
 template <int Q>
-hipError_t launch_shape(const ProductArgs& p, int shape, hipStream_t stream) {
+hipError_t launch_shape(const CodesArgs& p, int shape, hipStream_t stream) {
   return shape == kShapeHalf ? launch_codes<CodesHalf<Q>>(p, stream)
                              : launch_codes<CodesSmall<Q>>(p, stream);
 }
@@ -253,9 +253,9 @@ size_t codes_prepare_bytes(int64_t P, int G, int K, bool grouped, const ProductP
   return plan.shape == kShapeBig ? codes_area(P, G, K, grouped).total : 0;
 }
 
-hipError_t launch_product_fp8(const ProductArgs& p, const ProductPlan& plan, bool exact, void* area,
+hipError_t launch_product_fp8(const CodesArgs& p, const ProductPlan& plan, bool exact, void* area,
                               hipStream_t stream) {
-  ProductArgs q = p;
+  CodesArgs q = p;
   q.splits = plan.splits;
   q.cus = plan.cus;
   q.slices = plan.slices;
