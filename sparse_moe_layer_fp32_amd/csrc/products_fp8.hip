@@ -132,6 +132,7 @@ __device__ void list_row_tiles(const int32_t* __restrict__ offsets, int64_t P, i
   }
 }
 
+template <bool GATHER>
 __global__ __launch_bounds__(kPrepareThreads) void codes_prepare_kernel(
     const float* __restrict__ scales, const int32_t* __restrict__ row_ids, int row_div,
     int64_t x_rows, int64_t P, int steps, int64_t pitch, float* __restrict__ by_step,
@@ -146,17 +147,32 @@ __global__ __launch_bounds__(kPrepareThreads) void codes_prepare_kernel(
   }
   const int s0 = blockIdx.y * kTurnSteps;
   const int s = threadIdx.x % kTurnSteps;
+  // (loads without branches between them, so that they are under way together)
+  constexpr int STEP = kPrepareThreads / kTurnSteps, N = kTurnRows / STEP;
+  const int i0 = threadIdx.x / kTurnSteps;
+  int64_t src[N];
 #pragma unroll
-  for (int i = threadIdx.x / kTurnSteps; i < kTurnRows; i += kPrepareThreads / kTurnSteps) {
-    int64_t src = r0 + i < P ? r0 + i : -1;
-    if (src >= 0 && row_ids) {
-      const int id = row_ids[src];
-      src = id >= 0 && id / row_div < x_rows ? id / row_div : -1;
-    }
-    if (row_ids && s == 0 && blockIdx.y == 0)
-      sources[r0 + i] = src >= 0 ? static_cast<uint32_t>(src) * x_pitch : kFar;
-    tile[s][i] = src >= 0 && s0 + s < steps ? scales[src * steps + s0 + s] : 0.0f;
+  for (int n = 0; n < N; ++n) {
+    const int64_t r = r0 + i0 + n * STEP;
+    src[n] = GATHER ? row_ids[min(r, P - 1)] : r;
+    if (r >= P) src[n] = -1;
   }
+  if (GATHER)
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int id = static_cast<int>(src[n]);
+      src[n] = id >= 0 && id / row_div < x_rows ? id / row_div : -1;
+      if (s == 0 && blockIdx.y == 0)
+        sources[r0 + i0 + n * STEP] = src[n] >= 0 ? static_cast<uint32_t>(src[n]) * x_pitch : kFar;
+    }
+  float v[N] = {};
+  if (!GATHER || x_rows > 0)
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      v[n] = scales[max(src[n], int64_t(0)) * steps + min(s0 + s, steps - 1)];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    tile[s][i0 + n * STEP] = src[n] >= 0 && s0 + s < steps ? v[n] : 0.0f;
   __syncthreads();
   const int r = threadIdx.x % kTurnRows;
 #pragma unroll
@@ -191,7 +207,8 @@ hipError_t launch_run(CodesArgs p, char* area, hipStream_t stream) {
   uint32_t* const sources = reinterpret_cast<uint32_t*>(area + a.sources);
   const dim3 grid(static_cast<unsigned>(pitch / kTurnRows + (tiles ? 1 : 0)),
                   static_cast<unsigned>((steps + kTurnSteps - 1) / kTurnSteps));
-  codes_prepare_kernel<<<grid, kPrepareThreads, 0, stream>>>(
+  const auto prepare = p.src ? codes_prepare_kernel<true> : codes_prepare_kernel<false>;
+  prepare<<<grid, kPrepareThreads, 0, stream>>>(
       p.a_scale, p.src, p.row_div, p.x_rows, p.P, steps, pitch, by_step, p.offsets, p.G, tiles,
       a.most_tiles, num_tiles, sources, static_cast<uint32_t>(p.K) * 2);
   const hipError_t e = hipGetLastError();
