@@ -41,15 +41,19 @@ __global__ __launch_bounds__(64 * kThinWaves) void product_thin_fp8(CodesArgs p)
   const int fblocks = (p.F + 127) / 128;
   const float* ws = p.b_scale + (static_cast<int64_t>(un.g) * fblocks + un.col0 / 128) * blocks;
   const float* xs = p.a_scale + max(s, int64_t(0)) * blocks;
+  int none = 0;
+  asm volatile("" : "+v"(none));
   f32x4 acc{};
   for (int c0 = wid; c0 < blocks; c0 += kThinWaves * kThinAhead) {
     u32x4 wf[kThinAhead][2], xf[kThinAhead][2];
-    float scale[kThinAhead];
+    float wscale[kThinAhead], xscale[kThinAhead];
 #pragma unroll
     for (int i = 0; i < kThinAhead; ++i) {
       const int b = c0 + kThinWaves * i;
-      scale[i] = 0.0f;
-      if (b < blocks && s >= 0) scale[i] = ws[b] * xs[b];
+      // (by each lane: a scalar load would be waited for before the next loads)
+      wscale[i] = ws[min(b, blocks - 1) + none];
+      xscale[i] = 0.0f;
+      if (s >= 0) xscale[i] = xs[min(b, blocks - 1)];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int k = 64 * b + 16 * q + 8 * h;
@@ -60,6 +64,8 @@ __global__ __launch_bounds__(64 * kThinWaves) void product_thin_fp8(CodesArgs p)
     }
 #pragma unroll
     for (int i = 0; i < kThinAhead; ++i) {
+      const float scale =
+          c0 + kThinWaves * i < blocks && s >= 0 ? wscale[i] * xscale[i] : 0.0f;
       f32x4 t{};
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -69,7 +75,7 @@ __global__ __launch_bounds__(64 * kThinWaves) void product_thin_fp8(CodesArgs p)
               e4m3x8_to_bf16(wf[i][h][2 * d], wf[i][h][2 * d + 1]),
               e4m3x8_to_bf16(xf[i][h][2 * d], xf[i][h][2 * d + 1]), t, 0, 0, 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = fmaf(scale[i], t[j], acc[j]);
+      for (int j = 0; j < 4; ++j) acc[j] = fmaf(scale, t[j], acc[j]);
     }
   }
   // lane: row lane % 16, columns 4 (lane / 16) .. + 3
