@@ -478,7 +478,7 @@ moe_status moe_combine_forward(const moe_dispatch_config* cfg, const void* rows,
  *   drows[pair_pos[t][j]] = weights[t][j] dy[t]          or NULL
  *   dweights[t][j] = <dy[t], rows[pair_pos[t][j]]>       or NULL
  * rows is not read, and may be NULL, when dweights is NULL; weights may be NULL,
- * for ones. */
+ * for ones.  drows may be rows itself. */
 moe_status moe_combine_backward(const moe_dispatch_config* cfg, const void* dy, const void* rows,
                                 const int32_t* pair_pos, const float* weights, void* drows,
                                 float* dweights, hipStream_t stream);
@@ -516,7 +516,8 @@ moe_status moe_quantize_weight(int32_t num_groups, int32_t out_features, int32_t
  *   w  [G][F][K] codes, w_scales [G][ceil(F / 128)][ceil(K / 128)]
  * with their configurations, epilogues and limits (dw_dtype and accumulate are
  * not used), in_features a multiple of 16, and a workspace size of their own.
- * Codes of NaN make the results that they meet NaN.
+ * Codes of NaN make the results that they meet NaN.  The two scales of a block
+ * are multiplied first, in fp32.
  *
  * Sums.  fp32 results (y_dtype) are sums of exact products in fp32, each block's
  * times its two scales.  For bf16 results the codes are multiplied by the 8-bit

@@ -1,10 +1,17 @@
 // Large products of codes: blocks that stay on their CU and take one 256 x 256
 // tile after the other, for bf16 results.
 //
-// A tile of 32 steps by itself takes 58 us of steps and 15 of start and end: its
-// first loads find nothing to hide behind, and neither do its last stores.  Here
-// the rings run on across tiles: the last two steps of a tile load the first two
-// stages of the next, which arrive while the tile leaves.
+// A tile by itself starts with loads that have nothing to hide behind, and ends
+// with stores that have not either.  Here the rings run on across tiles: the last
+// two steps of a tile load the first two stages of the next, which arrive while the
+// tile leaves (8192 x 512 -> 8192, four steps a tile: 74 us, from 88; at 32 steps a
+// tile 1%).
+//
+// Bound: power and the matrix pipe.  8192 x 4096 -> 11264 takes 323 us here, 2.3
+// PFLOP/s, at 1.97 GHz (2.4 with operands of zeros); MFMA busy 57%, the additions
+// of blocks under their scales 12% of the cycles, tiles' ends 9%, loads 8%, LDS
+// reads 6%, the barrier in mid-step 3%.  Ragged products of few rows a group are
+// bound by memory: 65536 rows of 288 groups, 4096 -> 1280, move 2.7 GB in 460 us.
 //
 //  * Rings: three stages of x, two of W, all 160 KB.  A wave holds a step's
 //    fragments of W from the step's start, so W's slot is free after a barrier in
@@ -16,9 +23,9 @@
 //  * Waves take the 32-row blocks of a tile in turn (block b: wave row b % 2), so
 //    that a tile of fewer rows, a group's remainder or a cut tile, costs both
 //    waves of a SIMD as much less; rows outside the tile are not loaded.
-//  * The rows' scales come from a copy ordered by steps (scales_by_step), 128
+//  * The rows' scales come from a copy ordered by steps (codes_prepare_kernel), 128
 //    bytes to a load: read as they lie, 32 rows 128 bytes apart, they took as long
-//    to fetch as the panels (8192 x 4096 -> 11264: 421 us instead of 373).
+//    to fetch as the panels (13% of 8192 x 4096 -> 11264; the copy takes 5 us).
 #pragma once
 
 #include "codes_tile.h"

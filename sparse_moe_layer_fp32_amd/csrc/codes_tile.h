@@ -8,6 +8,11 @@
 //  * A step's products are summed on their own, and the sums added to the
 //    accumulators times the scales of their row and column block, in fp32: 16
 //    FMAs for every two products of 64 codes.  They run under the next products.
+//  * Widened codes are bound by the widening: each wave converts its 32 + 32 rows
+//    of a step for eight products of 32 x 32 x 16 (777 x 1296 -> 2056, 429 tiles of
+//    64 x 64: 14 us, MFMA busy 17%, waiting 33%).  Native 64 x 64 and 128 x 256
+//    tiles serve few rows, where W's stream bounds them (512 rows in 288 groups,
+//    4096 -> 1280: 139 us, 5.1 TB/s).
 //  * One loop serves all steps: loads of stages behind the last see an empty
 //    buffer.  (A second loop for the last steps costs registers that are not
 //    there: 128 accumulators, 32 sums, 48 of fragments.)

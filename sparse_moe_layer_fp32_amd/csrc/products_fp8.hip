@@ -19,7 +19,8 @@ namespace {
 // fragments, its codes and x's widened to bf16 on the way: the stream bounds it,
 // not the products, and their sums are exact for both types of y.  A wave takes
 // blocks of 128 codes in turn, 32 of each W row a lane; the four products of a
-// block start from zero and are added times its scales.
+// block start from zero and are added times its scales.  One row, 4096 -> 1280: 5.8
+// us (latency: 80 blocks, one turn of loads), 11264 -> 4096: 10.2, 4.5 TB/s.
 constexpr int kThinWaves = 8;
 constexpr int kThinAhead = 4;  // blocks that a wave requests before it multiplies
 

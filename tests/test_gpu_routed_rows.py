@@ -254,3 +254,18 @@ def test_experts_in_two_halves(moe, name):
     dw1, do1 = torch.empty(T, k, **F32), torch.empty(P, H, **F32)
     moe.moe_combine_backward(whole, dy, o, r.pos, r.gw, do1, dw1)
     assert torch.equal(dw, dw1) and torch.equal(do, do1)
+
+
+@pytest.mark.parametrize("T,k,H", [(5, 3, 264), (300, 8, 1024), (40, 2, 4096)])
+def test_row_gradients_in_place_of_the_rows(moe, T, k, H):
+    """drows may be rows itself: every row is read before it is written."""
+    P = T * k
+    cfg = moe.make_dispatch_config(T, P, k, H)
+    g = torch.Generator().manual_seed(T)
+    pos = torch.randperm(P, generator=g).view(T, k).int().cuda()
+    dy, o, w = pu.bf16(T, H, seed=1).cuda(), pu.bf16(P, H, seed=2).cuda(), pu.f32(T, k, seed=3).cuda()
+    do, dw = torch.empty(P, H, **BF), torch.empty(T, k, **F32)
+    moe.moe_combine_backward(cfg, dy, o, pos, w, do, dw)
+    dw2 = torch.empty(T, k, **F32)
+    moe.moe_combine_backward(cfg, dy, o, pos, w, o, dw2)
+    assert torch.equal(o, do) and torch.equal(dw2, dw)
