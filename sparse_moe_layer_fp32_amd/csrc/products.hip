@@ -336,30 +336,29 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
 }
 
 // Products of codes: the same estimate from figures of their own, fitted to the
-// times of 2140 products (2 to 16384 rows, 64 to 11264 features, 1 to 288 groups,
-// bf16 and fp32 results) in every shape and split: the choice is 1.7% slower than
-// the best measured on the mean; by the figures of the bf16 products it was 4.5%.
-// Steps are of 128 codes, of the thin kernel 4096.  `share`: the least part of a
-// tile that a group with rows has more than its rows fill.  No shape is faster
-// than the stream of its weights; of those that it bounds the one with the least
-// work is taken (512 rows in 288 groups, 4096 -> 1280: 143 us in Half or Small,
-// 153 in Big).  Big (with its prepare launch: kPrepare): bf16 results, in one
+// times of 3852 products (2 to 16384 rows, 64 to 11264 features, 1 to 288 groups,
+// bf16 and fp32 results) in every shape and split: the choice is 1.3% slower than
+// the best measured on the mean.  Steps are of 128 codes, of the thin kernel 4096.
+// `share`: the least part of a tile that a group with rows has more than its rows
+// fill.  No shape is faster than the stream of its weights; of those that it
+// bounds the one with the least work is taken (512 rows in 288 groups, 4096 ->
+// 1280: 130 us in Small, 142 in Half, 153 in Big).  Big: bf16 results, in one
 // range, of two steps or more.
 struct CodesCost {
   int per_cu;
   float full, partly, fixed, share;
 };
-constexpr CodesCost kCodesNative[] = {{1, 1.376f, 0.782f, 5.0f, 0.485f},
-                                      {1, 1.159f, 0.535f, 6.9f, 0.624f},
+constexpr CodesCost kCodesNative[] = {{1, 1.278f, 0.847f, 6.67f, 0.52f},
+                                      {1, 1.192f, 0.299f, 7.41f, 0.40f},
                                       {},
-                                      {2, 0.442f, 0.140f, 5.7f, 0.826f}};
+                                      {3, 0.370f, 0.155f, 5.73f, 1.18f}};
 constexpr CodesCost kCodesExact[] = {{},
-                                     {1, 1.368f, 0.989f, 6.3f, 0.624f},
+                                     {1, 1.025f, 0.635f, 9.20f, 0.32f},
                                      {},
-                                     {2, 0.525f, 0.202f, 5.4f, 0.826f}};
-constexpr CodesCost kCodesThin = {1, 2.685f, 0.337f, 2.46f, 0.334f};
-constexpr float kCodesFilling = 0.79f, kCodesJoin = 2.0f, kCodesJoinBytesPerUs = 11.5e6f;
-constexpr float kPrepare = 3.4f, kCodesBytesPerUs = 4.8e6f, kCodesBeyond = 0.105f;
+                                     {3, 0.480f, 0.238f, 4.27f, 1.03f}};
+constexpr CodesCost kCodesThin = {1, 2.879f, 0.741f, 0.50f, 0.58f};
+constexpr float kCodesFilling = 0.48f, kCodesBytesPerUs = 4.45e6f, kCodesBeyond = 0.112f;
+constexpr float kCodesJoin = 1.13f, kCodesRaggedJoin = 1.55f, kCodesJoinBytesPerUs = 6.96e6f;
 constexpr int64_t kCodesThinRows = 64;
 
 namespace {
@@ -389,7 +388,7 @@ float codes_us(const CodesCost& c, int64_t P, int G, int F, int64_t steps, Shape
       us += n * c.partly * (1.0f + kCodesFilling * rest / cus) + c.fixed;
   }
   if (splits > 1)
-    us += kCodesJoin + (G > 1 ? kRaggedJoin : 0.0f) +
+    us += kCodesJoin + (G > 1 ? kCodesRaggedJoin : 0.0f) +
           static_cast<float>(P) * F * (8.0f * splits + 4.0f) / kCodesJoinBytesPerUs;
   return us;
 }
@@ -409,8 +408,8 @@ ProductPlan product_fp8_plan(int64_t P, int G, int K, int F, int cus, bool exact
     for (int s : {kShapeThin8, kShapeThin16})
       consider(s, 1, codes_us(kCodesThin, P, G, F, (steps + 31) / 32, kShapeSizes[s], 1, cus));
   if (!exact && steps >= 2)
-    consider(kShapeBig, 1, kPrepare + codes_us(kCodesNative[kShapeBig], P, G, F, steps,
-                                               kShapeSizes[kShapeBig], 1, cus));
+    consider(kShapeBig, 1, codes_us(kCodesNative[kShapeBig], P, G, F, steps,
+                                    kShapeSizes[kShapeBig], 1, cus));
   for (int s : {kShapeHalf, kShapeSmall})
     for (int splits = 1; splits <= kFewSplits && splits <= steps; splits *= 2)
       consider(s, splits, codes_us((exact ? kCodesExact : kCodesNative)[s], P, G, F, steps,
