@@ -269,3 +269,28 @@ def test_row_gradients_in_place_of_the_rows(moe, T, k, H):
     dw2 = torch.empty(T, k, **F32)
     moe.moe_combine_backward(cfg, dy, o, pos, w, o, dw2)
     assert torch.equal(o, do) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("name", ["few_rows", "ragged", "many_rows"])
+def test_gradient_of_the_rows_in_codes(moe, name):
+    """The experts' input gradient is the grouped product of dy's codes and of the
+    weights' codes transposed, whose blocks of 128 x 128 keep their scales."""
+    r = Routed(moe, name)
+    H, E, I, P = r.H, r.E, r.I, r.P
+    w = Codes(moe, r.w[2])                       # [E][H][I]
+    wt = Codes.__new__(Codes)
+    wt.codes, wt.scales = w.codes.transpose(1, 2).contiguous(), w.scales.transpose(1, 2).contiguous()
+    do = pu.bf16(P, H, seed=3).cuda()
+    c, s = torch.empty(P, H, dtype=torch.uint8, device="cuda"), torch.empty(P, fu.blocks(H), **F32)
+    moe.moe_quantize_rows(moe.make_quantize_config(P, H), do, None, c, s)
+    for y_dtype, t in (("bf16", torch.bfloat16), ("f32", torch.float32)):
+        cfg = moe.make_grouped_config(P, E, H, I, y_dtype=y_dtype)
+        dh = torch.empty(P, I, dtype=t, device="cuda")
+        moe.moe_grouped_forward_fp8(cfg, c, s, None, r.offsets, wt.codes, wt.scales, None, dh,
+                                    moe.alloc_grouped_fp8_workspace(cfg))
+        check_product(dh, c, s, wt, r, y_dtype)
+        # against the gradient of the formula with the weights as coded: W^T dy
+        for e, i, j in r.groups():
+            want = fu.values(c[i:j], s[i:j], 1) @ fu.values(w.codes[e], w.scales[e], fu.BLOCK)
+            off = ((dh[i:j].double() - want).norm() / want.norm()).item()
+            assert off <= (2.0 ** -8 / 3 ** 0.5 + 1e-4 if y_dtype == "bf16" else 1e-5), (e, off)
