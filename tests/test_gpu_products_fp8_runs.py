@@ -183,3 +183,35 @@ def test_two_calls_at_once_and_in_graphs(moe, plan):  # noqa: F811
         torch.cuda.synchronize()
         for i in range(2):
             assert torch.equal(y[i], y[2 + i]) and torch.equal(y[i], y[4 + i])
+
+
+@pytest.mark.parametrize("P,K,F", [(40, 272, 72), (300, 272, 200), (6000, 400, 2056)])
+def test_captured_call_follows_its_offsets(moe, P, K, F):
+    """A captured product whose groups and sources change between replays."""
+    E, xr = 6, 500
+    xc, xs = (t.cuda() for t in fu.random_codes(xr, K))
+    wc, ws = (torch.stack(v).cuda() for v in zip(*(fu.random_codes(F, K, 128, e + 1) for e in range(E))))
+    cfg = moe.make_grouped_config(P, E, K, F, x_rows=xr)
+    work = [moe.alloc_grouped_fp8_workspace(cfg) for _ in range(2)]
+    ys = [torch.zeros(P, F, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ids = torch.zeros(P, dtype=torch.int32, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    moe.moe_grouped_forward_fp8(cfg, xc, xs, ids, off, wc, ws, None, ys[1], work[1])
+    torch.cuda.synchronize()
+    assert not ys[1].any()  # no group has rows
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_grouped_forward_fp8(cfg, xc, xs, ids, off, wc, ws, None, ys[0], work[0])
+    gen = torch.Generator().manual_seed(P)
+    for cuts in ([0, 0, 0, 0, P], [P, P, P, P, P], [P // 3, P // 3, P // 2, P - 1, P - 1], [1, 2, 3, 4, 5]):
+        off.copy_(torch.tensor([0] + cuts + [P], dtype=torch.int32))
+        ids.copy_(torch.randint(0, xr, (P,), generator=gen, dtype=torch.int32))
+        g.replay()
+        moe.moe_grouped_forward_fp8(cfg, xc, xs, ids, off, wc, ws, None, ys[1], work[1])
+        torch.cuda.synchronize()
+        assert torch.equal(*ys) and ys[0].abs().sum(1).min() > 0
+        e = next(i for i, c in enumerate(cuts + [P]) if c > 0)
+        n = min((cuts + [P])[e], 50)  # the first rows belong to the first group that has any
+        want = fu.values(xc[ids[:n].long()], xs[ids[:n].long()], 1) @ fu.values(wc[e], ws[e], fu.BLOCK).t()
+        off2 = ((ys[0][:n].double() - want).norm() / want.norm()).item()
+        assert off2 <= 2.0 ** -8 / 3 ** 0.5 + 1e-4
