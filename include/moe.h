@@ -525,8 +525,8 @@ moe_status moe_quantize_weight(int32_t num_groups, int32_t out_features, int32_t
  * what lies 2^-13 below the largest of the eight, and the runs in fp32: before
  * they are rounded, results are off by less than 2^-10 of the sum of the largest
  * terms of each run, and of normally distributed values by 1.4e-5 in the 2-norm,
- * which their rounding to 2^-8 hides.  Batches of few rows are summed exactly for
- * both.
+ * which their rounding to 2^-8 hides.  (Some sizes of few rows are summed as for
+ * fp32 results.)
  *
  * The gradient of x is the same product with the weights' transposed codes: a
  * block of 128 x 128 keeps its scale when it is transposed. */
