@@ -517,7 +517,8 @@ moe_status moe_quantize_weight(int32_t num_groups, int32_t out_features, int32_t
  * with their configurations, epilogues and limits (dw_dtype and accumulate are
  * not used), in_features a multiple of 16, and a workspace size of their own.
  * Codes of NaN make the results that they meet NaN.  The two scales of a block
- * are multiplied first, in fp32.
+ * are multiplied first, in fp32.  A row whose source lies outside x has codes and
+ * scales of 0, so that it too is NaN where a weight block's scale is not finite.
  *
  * Sums.  fp32 results (y_dtype) are sums of exact products in fp32, each block's
  * times its two scales.  For bf16 results the codes are multiplied by the 8-bit

@@ -65,8 +65,8 @@ __global__ __launch_bounds__(64 * kThinWaves) void product_thin_fp8(CodesArgs p)
     }
 #pragma unroll
     for (int i = 0; i < kThinAhead; ++i) {
-      const float scale =
-          c0 + kThinWaves * i < blocks && s >= 0 ? wscale[i] * xscale[i] : 0.0f;
+      // (0 for a row without a source, times W's scale: NaN where that is not finite)
+      const float scale = c0 + kThinWaves * i < blocks ? wscale[i] * xscale[i] : 0.0f;
       f32x4 t{};
 #pragma unroll
       for (int h = 0; h < 2; ++h)
