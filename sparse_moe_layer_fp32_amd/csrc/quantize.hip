@@ -148,7 +148,7 @@ hipError_t launch_quantize_rows(const uint16_t* x, const int32_t* pos, int64_t t
   const unsigned grid = static_cast<unsigned>((threads + kQuantThreads - 1) / kQuantThreads);
   // Codes that do not stay in the 256 MB last-level cache until they are read go
   // past it (8192 tokens of 4096 to 8 rows each: 55 us, from 70).
-  const bool past = rows * (cols + 4 * blocks) > (int64_t(256) << 20);
+  const bool past = rows_past_cache(tokens, rows, top_k, cols + 4 * blocks);
   if (past)
     quantize_rows_kernel<true><<<grid, kQuantThreads, 0, stream>>>(x, pos, tokens, rows, top_k, cols,
                                                                    blocks, codes, scales);

@@ -21,6 +21,9 @@ struct RowsArgs {
   float* dw;           // [tokens][top_k]
   int tok_f32, row_f32;
 };
+// Whether the rows that a call's pairs can name go past the last-level cache.
+bool rows_past_cache(int64_t tokens, int64_t rows, int top_k, int64_t row_bytes);
+
 // row_out[pos] = tok
 hipError_t launch_dispatch(const RowsArgs& p, hipStream_t stream);
 // tok_out = base + sum_j w row[pos]

@@ -13,6 +13,7 @@
 // gradients of 8191 x 3 rows of 7168: 147); a copy of 2 GiB 4.9.  Of few tokens,
 // latency: 5 x 8 rows of 4096 2.4 us, combine of 64 x 8 3.5.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "activation.h"
@@ -213,11 +214,10 @@ void with_types(const RowsArgs& p, F f) {
   }
 }
 
-// Rows that do not stay in the 256 MB last-level cache between their writer and
-// their reader go past it (8192 x 8 rows of 4096, 537 MB: the sum over slots 109
-// us, from 131, dispatch 108, from 118; 1024 x 8 rows, 67 MB: 17.8, from 14.7).
+// Sums of streamed rows are streamed too (8192 x 8 rows of 4096 into 67 MB: 100 us,
+// from 109 with sums that stay; with a kernel that reads them at once 128, 130).
 bool streams(const RowsArgs& p) {
-  return p.rows * p.hidden * (p.row_f32 ? 4 : 2) > (int64_t(256) << 20);
+  return rows_past_cache(p.tokens, p.rows, p.top_k, int64_t(p.hidden) * (p.row_f32 ? 4 : 2));
 }
 
 // Waves per token of the weights' gradient (us with 1 and 4, k = 8: 8192 x 256 20,
@@ -252,6 +252,15 @@ void with_constant(bool v, F f) {
   return hipGetLastError()
 
 }  // namespace
+
+// Rows that do not stay in the 256 MB last-level cache between their writer and
+// their reader go past it (8192 x 8 rows of 4096, 537 MB: the sum over slots 108
+// us, from 131, dispatch 109, from 118); others stay, whatever room the buffer has
+// (1024 x 8, 67 MB: dispatch and a kernel that reads the rows 34.0 us, past the cache
+// 39.1; the gradients 24.2 and 29.1; the sum by itself 14.7 either way).
+bool rows_past_cache(int64_t tokens, int64_t rows, int top_k, int64_t row_bytes) {
+  return std::min(rows, tokens * top_k) * row_bytes > (int64_t(256) << 20);
+}
 
 hipError_t launch_dispatch(const RowsArgs& p, hipStream_t stream) {
   if (p.tokens == 0 || p.rows == 0) return hipSuccess;
