@@ -289,9 +289,9 @@ moe_status moe_dense_forward(const moe_dense_config* cfg, const uint16_t* x,
  * group sizes, SwiGLU between an expert's products, and the gradients of all
  * three.  A routed layer in training is moe_route, moe_permute, grouped gate
  * and up products of the gathered tokens, moe_swiglu_forward, and the grouped
- * down product; the experts' backward pass is the same calls backwards, and
- * the gradients of the combine and the router and the sum of dx over a token's
- * rows are the caller's.
+ * down product, and moe_combine_forward; its backward pass is the same calls
+ * backwards, with moe_dispatch_backward for the sum of dx over a token's rows.  The
+ * router's gradient is the caller's.
  *
  * Conventions and errors as above, and:
  *   - bf16 operands, exact products, fp32 accumulation; bias and its gradient
@@ -489,8 +489,9 @@ moe_status moe_combine_backward(const moe_dispatch_config* cfg, const void* dy, 
  * last block of a row, or of a column of blocks, may be smaller.  The value of a
  * code is decode(code) * scale.  Rounding a block v to codes:
  *   a = max(largest |v|, 2^-90);  scale = a / 448;  code = e4m3(v * (448 / a)),
- * to nearest even.  A block that holds a NaN or an infinity has that for its
- * scale. */
+ * to nearest even, with the scale, 448 / a and its product with v rounded to fp32
+ * (so that a value within 2^-22 of itself of the middle between two codes may get
+ * either).  A block that holds a NaN or an infinity has that for its scale. */
 typedef struct {
   int64_t tokens;   /* rows of x, >= 0                                       */
   int64_t rows;     /* rows of codes and scales, >= 0                        */
@@ -506,7 +507,7 @@ moe_status moe_quantize_rows(const moe_quantize_config* cfg, const uint16_t* x,
                              hipStream_t stream);
 
 /* codes [G][F][K] and scales [G][ceil(F / 128)][ceil(K / 128)] of w [G][F][K] bf16.
- * K is a multiple of 16, at most 2^21 blocks. */
+ * K is a multiple of 16; F and K are up to 65536, and at most 2^21 blocks. */
 moe_status moe_quantize_weight(int32_t num_groups, int32_t out_features, int32_t in_features,
                                const uint16_t* w, uint8_t* codes, float* scales,
                                hipStream_t stream);

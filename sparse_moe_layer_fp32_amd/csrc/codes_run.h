@@ -10,8 +10,11 @@
 // Bound: power and the matrix pipe.  8192 x 4096 -> 11264 takes 323 us here, 2.3
 // PFLOP/s, at 1.97 GHz (2.4 with operands of zeros); MFMA busy 57%, the additions
 // of blocks under their scales 12% of the cycles, tiles' ends 9%, loads 8%, LDS
-// reads 6%, the barrier in mid-step 3%.  Ragged products of few rows a group are
-// bound by memory: 65536 rows of 288 groups, 4096 -> 1280, move 2.7 GB in 460 us.
+// reads 6%, the barrier in mid-step 3%.  Gathered rows of few a group take longer:
+// 65536 rows of 288 groups, 4096 -> 1280, 466 us, MFMA busy 45%.  Their L2s fetch 2.5
+// GB, of which memory has to give W's 1.5 (x's 34 MB stay in the last-level cache),
+// and the compiler holds x's buffer in vector registers: each of its loads runs in a
+// loop that makes it scalar, four a step, and 13 vector registers are spilled.
 //
 //  * Rings: three stages of x, two of W, all 160 KB.  A wave holds a step's
 //    fragments of W from the step's start, so W's slot is free after a barrier in

@@ -10,15 +10,14 @@
 //    FMAs for every two products of 64 codes.  They run under the next products.
 //  * Widened codes are bound by the widening: each wave converts its 32 + 32 rows
 //    of a step for eight products of 32 x 32 x 16 (777 x 1296 -> 2056, 429 tiles of
-//    64 x 64: 13.8 us, MFMA busy 17%, waiting 33%).  Native 64 x 64 and 128 x 256
+//    64 x 64: 12.9 us, MFMA busy 17%, waiting 36%).  Native 64 x 64 and 128 x 256
 //    tiles serve few rows, where W's stream bounds them (512 rows in 288 groups,
 //    4096 -> 1280: 130 us, 5.4 TB/s).
 //  * 64 x 64 tiles have three stages, so that three blocks share a CU (there 141 us
-//    with four stages and two blocks, 140 with two and five; 2048 rows: 261, 283 and
+//    with four stages and two blocks, 140 with two and four; 2048 rows: 261, 283 and
 //    284; 8 rows in 8 groups, where a CU has one block: 14.4, 14.0 and 22.5).
 //  * One loop serves all steps: loads of stages behind the last see an empty
-//    buffer.  (A second loop for the last steps costs registers that are not
-//    there: 128 accumulators, 32 sums, 48 of fragments.)
+//    buffer and bring zeros without touching memory.
 #pragma once
 
 #include <algorithm>

@@ -339,8 +339,9 @@ ProductPlan product_plan(int op, int64_t P, int G, int K, int F, int cus) {
 // times of 3852 products (2 to 16384 rows, 64 to 11264 features, 1 to 288 groups,
 // bf16 and fp32 results) in every shape and split: the choice is 1.3% slower than
 // the best measured on the mean.  Steps are of 128 codes, of the thin kernel 4096.
-// `share`: the least part of a tile that a group with rows has more than its rows
-// fill.  No shape is faster than the stream of its weights; of those that it
+// `share`: the least part of a tile that a group with rows is charged beyond what its
+// rows fill, a weight of the fit like the others, and so above 1 for the small tiles.
+// No shape is faster than the stream of its weights; of those that it
 // bounds the one with the least work is taken (512 rows in 288 groups, 4096 ->
 // 1280: 130 us in Small, 142 in Half, 153 in Big).  Big: bf16 results, in one
 // range, of two steps or more.

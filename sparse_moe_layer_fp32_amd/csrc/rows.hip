@@ -8,10 +8,11 @@
 // Bound: HBM.  All four walk the tokens, so that a token's own row is read or
 // written once, whatever top_k is, and every row of an expert once.  Sums are
 // formed in fp32 in slot order.  A lane takes 8 columns of a token.  Bytes needed
-// over time: 6.2 TB/s (sum over 8192 x 8 rows of 4096, base added: 109 us), 5.6
-// (combine of 32768 x 8 pairs, half of them with rows, into fp32: 286 us; its
+// over time: 6.2 TB/s (sum over 8192 x 8 rows of 4096, base added: 109 us), 5.7
+// (combine of 32768 x 8 pairs, half of them with rows, into fp32: 285 us; its
 // gradients of 8191 x 3 rows of 7168: 147); a copy of 2 GiB 4.9.  Of few tokens,
-// latency: 5 x 8 rows of 4096 2.4 us, combine of 64 x 8 3.5.
+// latency: 5 x 8 rows of 4096 2.5 us, combine of 64 x 8 3.6, its gradients 7.5, one
+// after the other in a graph (alone 3.0 and 4.2, traced).
 
 #include <algorithm>
 #include <type_traits>
