@@ -288,8 +288,8 @@ moe_status moe_dense_forward(const moe_dense_config* cfg, const uint16_t* x,
  * and residual in its epilogue, the same map grouped by expert with ragged
  * group sizes, SwiGLU between an expert's products, and the gradients of all
  * three.  A routed layer in training is moe_route, moe_permute, grouped gate
- * and up products of the gathered tokens, moe_swiglu_forward, and the grouped
- * down product, and moe_combine_forward; its backward pass is the same calls
+ * and up products of the gathered tokens, moe_swiglu_forward, the grouped down
+ * product, and moe_combine_forward; its backward pass is the same calls
  * backwards, with moe_dispatch_backward for the sum of dx over a token's rows.  The
  * router's gradient is the caller's.
  *
